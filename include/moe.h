@@ -376,6 +376,83 @@ int moe_forward_noalloc(const moe_dims_t* dims, moe_path_t path, const uint16_t*
                         const int32_t* rep_count, const int32_t* rep_slots, int32_t* load_hist, uint16_t* out,
                         moe_path_t* chosen, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear operators: the fp8 product with an f32 scale per block of 128 (the
+ * format of fp8 checkpoints' dense, shared-expert and routed-expert layers),
+ * the quantiser in front of it, and the 16-bit products grouped by expert
+ * with both gradients (fine-tuning of unquantised experts).
+ *
+ * Groups.  Weights hold `groups` matrices [N, K]; rows [offsets[g],
+ * offsets[g+1]) of the row tensors belong to matrix g.  offsets: DEVICE i32
+ * [groups + 1], ascending, within [0, rows] (the caller's contract; entries
+ * outside are clamped, so nothing outside the tensors is touched).  NULL is
+ * allowed for groups == 1 and means all rows.  Groups may be empty.  Rows in
+ * no group are not written by the row products.  moe_quant_permute's
+ * `offsets` are such offsets.
+ * Sums and scales are f32; each output is rounded once, to nearest even.
+ * Results do not depend on timing: there are no atomic sums.
+ * Conventions as above (device pointers, 16-byte alignment, asynchronous on
+ * `stream`, nothing allocated, host validation first).  rows == 0 is valid;
+ * row tensors may then be NULL.  Outputs must not overlap inputs.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  MOE_TYPE_BF16 = 0,
+  MOE_TYPE_F16 = 1,
+  MOE_TYPE_F32 = 2,
+  MOE_TYPE_FP8 = 3 /* e4m3fn codes */
+} moe_type_t;
+
+/* Limits: 0 <= rows <= 1<<20, 1 <= N, K <= 32768, 1 <= groups <= 1024.
+ * in_type FP8: K a multiple of 16, any N, out_type BF16, F16 or F32.
+ * in_type BF16 or F16: K a multiple of 8 (and N for the gradients), out_type
+ * in_type or F32. */
+typedef struct {
+  int32_t rows, N, K, groups;
+  int32_t in_type, out_type; /* moe_type_t */
+} moe_linear_t;
+
+/* Workspace bytes of any linear call on these sizes, the gradients included
+ * (independent of out_type).  May be 0; returns 0 for invalid sizes too. */
+size_t moe_linear_workspace_bytes(const moe_linear_t* d);
+
+/* q u8 [rows, K] = e4m3_rne(x * (1 / s)), qs f32 [rows, ceil(K/128)]:
+ * s = max(amax / 448, 2^-126) over the row's block of 128 columns (the last
+ * one may be shorter), all in f32.  x: BF16, F16 or F32 (x_type) [rows, K], ldx
+ * elements between rows; K and ldx multiples of 16 (K at most 32768).  A block
+ * holding a NaN gets a NaN scale and NaN codes; one holding an infinity an
+ * infinite scale, zero codes and NaN at the infinity. */
+int moe_fp8_quant(int32_t rows, int32_t K, int32_t x_type, const void* x, int64_t ldx, uint8_t* q, float* qs,
+                  moe_stream_t stream);
+
+/* The same of h = silu(x[:, :K]) * x[:, K:2K] in f32; x [rows, 2K], ldx >= 2K. */
+int moe_fp8_swiglu_quant(int32_t rows, int32_t K, int32_t x_type, const void* x, int64_t ldx, uint8_t* q, float* qs,
+                         moe_stream_t stream);
+
+/* y[r, n] = sum over blocks b of 128 columns of
+ *   xs[r, b] * ws[g, n/128, b] * sum_{k in b} xq[r, k] w[g, n, k].
+ * xq u8 [rows, K], xs f32 [rows, ceil(K/128)], w u8 [groups, N, K], ws f32
+ * [groups, ceil(N/128), ceil(K/128)], y [rows, N] of out_type.  d->in_type FP8.
+ * Inside a block the matrix instruction aligns 32 products to the largest of
+ * them and keeps about 14 bits below its leading one; everything after is f32. */
+int moe_fp8_linear(const moe_linear_t* d, const uint8_t* xq, const float* xs, const uint8_t* w, const float* ws,
+                   const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* y[r, n] = sum_k x[r, k] w[g, n, k]: x [rows, K] and w [groups, N, K] of
+ * in_type, y [rows, N] of out_type. */
+int moe_grouped_linear(const moe_linear_t* d, const void* x, const void* w, const int32_t* offsets, void* y,
+                       void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Gradient of the rows: dx[r, k] = sum_n dy[r, n] w[g, n, k]; dy [rows, N] of
+ * in_type, dx [rows, K] of out_type. */
+int moe_grouped_linear_dx(const moe_linear_t* d, const void* dy, const void* w, const int32_t* offsets, void* dx,
+                          void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Gradient of the weights: dw[g, n, k] = sum over the group's rows of
+ * dy[r, n] x[r, k] (zeros for an empty group); dw [groups, N, K] of out_type,
+ * overwritten. */
+int moe_grouped_linear_dw(const moe_linear_t* d, const void* dy, const void* x, const int32_t* offsets, void* dw,
+                          void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

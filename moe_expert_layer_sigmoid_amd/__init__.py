@@ -32,7 +32,9 @@ EXPORTS = ("moe_workspace_bytes", "moe_select_path", "moe_status_string", "moe_p
            "moe_grouped_gemm2_combine", "moe_grouped_gemm1_swiglu_pairs", "moe_grouped_gemm2_combine_pairs",
            "moe_forward", "moe_eplb_rebalance", "moe_eplb_migrate",
            "moe_router_workspace_bytes", "moe_router_logits", "moe_forward_small_m",
-           "moe_a16w4_workspace_bytes", "moe_forward_a16w4", "moe_forward_noalloc", "moe_replica_of")
+           "moe_a16w4_workspace_bytes", "moe_forward_a16w4", "moe_forward_noalloc", "moe_replica_of",
+           "moe_linear_workspace_bytes", "moe_fp8_quant", "moe_fp8_swiglu_quant", "moe_fp8_linear",
+           "moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw")
 
 
 class MoeError(RuntimeError):
@@ -55,6 +57,27 @@ class Dims(ctypes.Structure):
         vals = {f: getattr(d, f, 0) for f, _ in cls._fields_}
         vals.update(kw)
         return cls(**{k: int(v) for k, v in vals.items()})
+
+
+TYPES = {"bf16": 0, "f16": 1, "f32": 2, "fp8": 3}   # moe_type_t
+_TORCH_TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn)
+
+
+class Linear(ctypes.Structure):
+    """moe_linear_t"""
+    _fields_ = [("rows", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("in_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+    def __init__(self, rows: int, N: int, K: int, groups: int = 1, in_type: str = "bf16",
+                 out_type: Optional[str] = None):
+        """``in_type`` / ``out_type``: "bf16", "f16", "f32", "fp8"; the output
+        defaults to in_type (bf16 for fp8)."""
+        if out_type is None:
+            out_type = "bf16" if in_type == "fp8" else in_type
+        for n, t in (("in_type", in_type), ("out_type", out_type)):
+            if t not in TYPES:
+                raise ValueError(f"{n}: {t!r} is none of {', '.join(TYPES)}")
+        super().__init__(int(rows), int(N), int(K), int(groups), TYPES[in_type], TYPES[out_type])
 
 
 class Taps(ctypes.Structure):
@@ -122,6 +145,18 @@ def lib() -> ctypes.CDLL:
         L.moe_replica_of.restype = ctypes.c_int32
         L.moe_eplb_rebalance.argtypes = [I, I, I, I, P, P, P, P, P]
         L.moe_eplb_migrate.argtypes = [D, P, I, P, P, P, P, P, P, P, P, P]
+        N = ctypes.POINTER(Linear)
+        S = ctypes.c_size_t
+        L.moe_linear_workspace_bytes.argtypes = [N]
+        L.moe_linear_workspace_bytes.restype = S
+        for n in ("moe_fp8_quant", "moe_fp8_swiglu_quant"):
+            getattr(L, n).argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64, P, P, P]
+            getattr(L, n).restype = I
+        L.moe_fp8_linear.argtypes = [N, P, P, P, P, P, P, P, S, P]
+        L.moe_fp8_linear.restype = I
+        for n in ("moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw"):
+            getattr(L, n).argtypes = [N, P, P, P, P, P, S, P]
+            getattr(L, n).restype = I
         for n in ("moe_pack_weights", "moe_route", "moe_eplb_remap_record", "moe_quant_permute",
                   "moe_grouped_gemm1_swiglu", "moe_grouped_gemm2_combine", "moe_grouped_gemm1_swiglu_pairs",
                   "moe_grouped_gemm2_combine_pairs", "moe_forward", "moe_eplb_rebalance", "moe_eplb_migrate"):
@@ -480,3 +515,123 @@ def moe_forward_a16w4(d: Dims, x, logits, pw1, pw1s, pw2, pw2s, rep_count, rep_s
         _ptr(act, "act", _bf16(act), TMK * d.F) if act is not None else None,
         _ptr(ws, "workspace", u8), ws.numel(), _stream(stream))
     _check("moe_forward_a16w4", rc)
+
+
+# ----------------------------------------------------------------------------
+# Linear operators: fp8 with a scale per block of 128, 16-bit by expert
+# ----------------------------------------------------------------------------
+
+def moe_linear_workspace_bytes(d: Linear) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(d)))
+
+
+def linear_workspace(d: Linear, device="cuda") -> torch.Tensor:
+    """A workspace for every linear call on ``d``'s sizes, the gradients included."""
+    return torch.empty(max(moe_linear_workspace_bytes(d), 256), dtype=u8, device=device)
+
+
+def _addr(t: torch.Tensor, name: str, dtype, numel_min: int, dev) -> int:
+    """_ptr for the linear operators, whose smallest calls take a few us: the
+    address as an int, and every tensor on the same device as the first."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype and not (dtype is torch.float8_e4m3fn and t.dtype is u8):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, must be on one device (the first tensor is on {dev})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.numel() < numel_min:
+        raise ValueError(f"{name}: {t.numel()} elements, need at least {numel_min}")
+    return t.data_ptr()
+
+
+def _launch(fn: str, dev: torch.device, stream, *args) -> None:
+    """Call ``fn`` on the tensors' device, on its current stream by default."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    rc = getattr(lib(), fn)(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _fp8_quant(fn: str, x, q, qs, parts: int, stream) -> None:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x: expected a torch.Tensor of two dimensions")
+    rows, K = x.shape[0], x.shape[1] // parts
+    if x.device.type != "cuda":
+        raise ValueError("x: must be a device tensor")
+    if x.dtype not in _TORCH_TYPES[:3]:
+        raise TypeError(f"x: dtype {x.dtype}, expected bfloat16, float16 or float32")
+    if x.shape[1] != parts * K or (x.stride(1) != 1 and x.numel()):
+        raise ValueError("x: the columns must be contiguous" + (" and even in number" if parts == 2 else ""))
+    ldx = x.stride(0) if rows > 1 else parts * K
+    if ldx < parts * K:
+        raise ValueError("x: the rows must not overlap")
+    dev = x.device
+    _launch(fn, dev, stream, rows, K, _TORCH_TYPES.index(x.dtype), x.data_ptr(), ldx,
+            _addr(q, "q", torch.float8_e4m3fn, rows * K, dev), _addr(qs, "qs", f32, rows * _blocks(K), dev))
+
+
+def moe_fp8_quant(x, q, qs, stream=None) -> None:
+    """q (float8_e4m3fn or uint8 [rows, K]) and qs (float32 [rows,
+    ceil(K/128)]) of x [rows, K] (bfloat16, float16 or float32; rows may be
+    further apart than K elements)."""
+    _fp8_quant("moe_fp8_quant", x, q, qs, 1, stream)
+
+
+def moe_fp8_swiglu_quant(x, q, qs, stream=None) -> None:
+    """The same of silu(gate) * up, x [rows, 2K] holding gate | up."""
+    _fp8_quant("moe_fp8_swiglu_quant", x, q, qs, 2, stream)
+
+
+def _offsets(d: Linear, offsets, dev):
+    return None if offsets is None else _addr(offsets, "offsets", i32, d.groups + 1, dev)
+
+
+def _scratch(ws, dev):
+    return (None, 0) if ws is None else (_addr(ws, "workspace", u8, 0, dev), ws.numel())
+
+
+def moe_fp8_linear(d: Linear, xq, xs, w, ws, y, scratch, offsets=None, stream=None) -> None:
+    """y [rows, N] of fp8 rows xq [rows, K] with scales xs [rows, ceil(K/128)]
+    and fp8 weights w [groups, N, K] with scales ws [groups, ceil(N/128),
+    ceil(K/128)]; ``offsets`` int32 [groups + 1] on the device (None: one
+    group of all rows)."""
+    dev = w.device
+    _launch("moe_fp8_linear", dev, stream, ctypes.byref(d),
+            _addr(xq, "xq", torch.float8_e4m3fn, d.rows * d.K, dev), _addr(xs, "xs", f32, d.rows * _blocks(d.K), dev),
+            _addr(w, "w", torch.float8_e4m3fn, d.groups * d.N * d.K, dev),
+            _addr(ws, "ws", f32, d.groups * _blocks(d.N) * _blocks(d.K), dev), _offsets(d, offsets, dev),
+            _addr(y, "y", _TORCH_TYPES[d.out_type], d.rows * d.N, dev), *_scratch(scratch, dev))
+
+
+def _grouped(fn, d: Linear, a, an, a_name, b, bn, b_name, out, on, out_name, scratch, offsets, stream) -> None:
+    dev = out.device
+    t = _TORCH_TYPES[d.in_type]
+    _launch(fn, dev, stream, ctypes.byref(d), _addr(a, a_name, t, an, dev), _addr(b, b_name, t, bn, dev),
+            _offsets(d, offsets, dev), _addr(out, out_name, _TORCH_TYPES[d.out_type], on, dev),
+            *_scratch(scratch, dev))
+
+
+def moe_grouped_linear(d: Linear, x, w, y, scratch, offsets=None, stream=None) -> None:
+    """y [rows, N] = x [rows, K] times each group's w [N, K] transposed."""
+    _grouped("moe_grouped_linear", d, x, d.rows * d.K, "x", w, d.groups * d.N * d.K, "w", y, d.rows * d.N, "y",
+             scratch, offsets, stream)
+
+
+def moe_grouped_linear_dx(d: Linear, dy, w, dx, scratch, offsets=None, stream=None) -> None:
+    """dx [rows, K] = dy [rows, N] times each group's w [N, K]."""
+    _grouped("moe_grouped_linear_dx", d, dy, d.rows * d.N, "dy", w, d.groups * d.N * d.K, "w", dx, d.rows * d.K, "dx",
+             scratch, offsets, stream)
+
+
+def moe_grouped_linear_dw(d: Linear, dy, x, dw, scratch, offsets=None, stream=None) -> None:
+    """dw [groups, N, K]: per group, dy [rows, N] transposed times x [rows, K]; zeros for an empty group."""
+    _grouped("moe_grouped_linear_dw", d, dy, d.rows * d.N, "dy", x, d.rows * d.K, "x", dw, d.groups * d.N * d.K, "dw",
+             scratch, offsets, stream)
