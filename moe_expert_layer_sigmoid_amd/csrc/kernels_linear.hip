@@ -15,6 +15,7 @@
 
 #include <hip/hip_runtime.h>
 
+
 #include <type_traits>
 
 #include "linear_internal.hpp"
@@ -26,8 +27,19 @@ namespace {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 64;       // columns and rows of a block's output tile
-constexpr int kPitch = 128 + 16;  // bytes of a staged row: 128 of data, padded against bank conflicts
+constexpr int kXcd = 8;  // accelerator dies; block b runs on die b % 8, each has its own L2
+
+// LDS pointers.  The DMA target and the tiles being read are passed to one
+// inlined function as __restrict__: the compiler then knows that a read does
+// not depend on the DMA in flight and places no wait between them.
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) v4i lds_v4i;
+typedef __attribute__((address_space(3))) float lds_f32;
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) void* lds_void;
+
+constexpr uint32_t kOob = 0x80000000u;  // a buffer offset past every buffer used here: the load gives zeros
 
 template <int IN>
 __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {  // 16x16x32, 16-bit types
@@ -40,13 +52,6 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {  // 16x16x32, 16-bi
 // 16x16x128 of e4m3 operands, no block scales
 __device__ __forceinline__ v4f mfma8(v8i a, v8i b, v4f c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kFmtFp8, kFmtFp8, 0, 0, 0, 0);
-}
-
-template <int OUT>
-__device__ __forceinline__ void store1(void* out, size_t i, float v) {  // one rounding to the output type, to nearest even
-  if constexpr (OUT == kBF16) static_cast<__bf16*>(out)[i] = (__bf16)v;
-  else if constexpr (OUT == kF16) static_cast<_Float16*>(out)[i] = (_Float16)v;
-  else static_cast<float*>(out)[i] = v;
 }
 
 // Rows [lo, hi) of group g.  Offsets outside [0, rows], or falling, break the
@@ -78,8 +83,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int groups, int ro
     const unsigned long long past = __ballot(base + incl > tile);
     if (past) {
       const int l = __ffsll(past) - 1;
-      g = c + l;
-      t = tile - base - __shfl(incl - nt, l);
+      g = __builtin_amdgcn_readfirstlane(c + l);
+      t = __builtin_amdgcn_readfirstlane(tile - base - __shfl(incl - nt, l));
       return true;
     }
     base += __shfl(incl, 63);
@@ -87,157 +92,482 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int groups, int ro
   return false;
 }
 
-template <int IN, int OP, int OUT>
-__global__ void __launch_bounds__(256) k_linear(LinearArgs p) {
-  constexpr int ES = IN == kFP8 ? 1 : 2;
-  constexpr int RE = 128 / ES;  // reduction elements per stage
-  __shared__ __align__(16) uint8_t sa[kTile * kPitch], sb[kTile * kPitch];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l16 = lane & 15, q = lane >> 4;
-  const int wa = wave & 1, wb = wave >> 1;
-  const int cols = OP == kFwd ? p.N : p.K;
-  const int c0 = blockIdx.x * kTile;
-
-  // the tile's output rows and its reduction
-  int g, r0, nr, nred;
-  size_t out0;             // output index of the tile's (row 0, column 0)
-  int lo, hi;
-  if (OP == kDw) {
-    g = blockIdx.z;
-    group_rows(p.off, g, p.rows, lo, hi);
-    r0 = blockIdx.y * kTile;
-    nr = min(kTile, p.N - r0);
-    nred = hi - lo;
-    out0 = ((size_t)g * p.N + r0) * p.K + c0;
-  } else {
-    int t;
-    if (!find_tile<kTile>(p.off, p.groups, p.rows, blockIdx.y, g, t)) return;  // whole block
-    group_rows(p.off, g, p.rows, lo, hi);
-    r0 = lo + t * kTile;
-    nr = min(kTile, hi - r0);
-    nred = OP == kFwd ? p.K : p.N;
-    out0 = (size_t)r0 * cols + c0;
+// Row tiles of all groups.
+template <int TB>
+__device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int rows) {
+  int n = 0;
+  for (int c = threadIdx.x & 63; c < groups; c += 64) {
+    int lo, hi;
+    group_rows(off, c, rows, lo, hi);
+    n += (hi - lo + TB - 1) / TB;
   }
-  const uint8_t* wslab = static_cast<const uint8_t*>(p.a) + (OP == kDw ? 0 : (size_t)g * p.N * p.K * ES);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+  return __builtin_amdgcn_readfirstlane(n);
+}
 
-  // 16-byte piece `pc` of stage row `row` of an operand with a contiguous reduction
-  auto stage_kc = [&](uint8_t* s, const uint8_t* src, int ld, int nrow, int e0) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int i = tid + 256 * m, row = i >> 3, pc = i & 7;
-      const int e = e0 + pc * (16 / ES);
-      v4i v = {0, 0, 0, 0};
-      if (row < nrow && e < nred) v = *reinterpret_cast<const v4i*>(src + ((size_t)row * ld + e) * ES);
-      *reinterpret_cast<v4i*>(s + row * kPitch + pc * 16) = v;
-    }
-  };
-  // ... and of one whose columns are contiguous: 8 columns of reduction row `red`
-  auto stage_mc = [&](uint8_t* s, const uint16_t* src, int ld, int ncol, int e0) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int i = tid + 256 * m, red = i >> 3, c = (i & 7) * 8;
-      v4i v = {0, 0, 0, 0};
-      if (c < ncol && e0 + red < nred) v = *reinterpret_cast<const v4i*>(src + (size_t)(e0 + red) * ld + c);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint16_t*>(s + (c + j) * kPitch + 2 * red) = (uint16_t)((uint32_t)v[j >> 1] >> (16 * (j & 1)));
-    }
-  };
+// Shape of a block's work.  TA x TB: columns x rows of its output tile; WA x WB
+// waves; NS: stages of the LDS ring; OCC: blocks per compute unit the
+// registers must allow.
+template <int IN_, int OP_, int TA_, int TB_, int WA_, int WB_, int NS_, int OCC_>
+struct Shape {
+  static constexpr int IN = IN_, OP = OP_, TA = TA_, TB = TB_, WA = WA_, WB = WB_, NS = NS_, OCC = OCC_;
+  static constexpr int W = WA * WB;
+  static constexpr int ES = IN == kFP8 ? 1 : 2;
+  static constexpr int RE = 128 / ES;               // reduction elements per stage
+  static constexpr bool AT = OP != kFwd;            // operand stored with its columns contiguous (read transposed)
+  static constexpr bool BT = OP == kDw;
+  static constexpr int TI = TA / WA / 16, TJ = TB / WB / 16;  // 16 x 16 tiles per wave
+  static constexpr int PG = TI < 4 ? TI : 4;        // A tiles whose columns interleave (below)
+  static constexpr int PGS = 4 * PG;
+  static constexpr int NA = TA / 8 / W, NB = TB / 8 / W;      // 1 KB DMA instructions per wave and stage
+  static constexpr int NI = NA + NB + (IN == kFP8 ? 1 : 0);
+  static constexpr int kScale = IN == kFP8 ? W * 256 : 0;
+  static constexpr int kSlot = (TA + TB) * 128 + kScale;
+  static constexpr int PRE = NS - 1;
+  static_assert(NA * W * 8 == TA && NB * W * 8 == TB && TI * WA * 16 == TA && TJ * WB * 16 == TB, "tile shape");
+  static_assert(PRE * NI < 64, "vmcnt range");
+  static_assert(IN != kFP8 || TB / 64 < W, "a wave for the weight scales");
+  static_assert(NS * kSlot <= 160 * 1024, "LDS");
+};
 
-  v4f acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
-  for (int e0 = 0; e0 < nred; e0 += RE) {
-    if (OP == kFwd) {
-      stage_kc(sa, wslab + (size_t)c0 * p.K * ES, p.K, p.N - c0, e0);
-      stage_kc(sb, static_cast<const uint8_t*>(p.b) + (size_t)r0 * p.K * ES, p.K, nr, e0);
-    } else if (OP == kDx) {
-      stage_mc(sa, reinterpret_cast<const uint16_t*>(wslab) + c0, p.K, cols - c0, e0);
-      stage_kc(sb, static_cast<const uint8_t*>(p.b) + (size_t)r0 * p.N * ES, p.N, nr, e0);
+struct Plan {
+  int nca;       // column tiles
+  int nrb;       // row tiles: kDw: of N; else an upper bound over all groups
+  int splits;    // ranges of the reduction, each by its own block into its own partial sums
+  int sps;       // stages per split (kFwd, kDx; kDw divides each group's own stages)
+  int out_type;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearArgs p, Plan pl) {
+  constexpr int TA = C::TA, TB = C::TB, TI = C::TI, TJ = C::TJ, W = C::W, ES = C::ES, NS = C::NS, PRE = C::PRE;
+  constexpr int IN = C::IN, OP = C::OP;
+  __shared__ __align__(1024) uint8_t ring[NS * C::kSlot];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int wa = wave % C::WA, wb = wave / C::WA;
+  const int cols = OP == kFwd ? p.N : p.K;
+
+  // ---- the block's tile.  Consecutive items share an XCD: inside a group,
+  // bands of four column tiles, row by row, so that the 32 tiles a die works
+  // on at one time read about 4 column and 8 row operands.
+  int g, lo, hi, c0, r0, nr, nred, split;
+  size_t out0;
+  {
+    const int xcd = blockIdx.x % kXcd, j = blockIdx.x / kXcd;
+    if (OP == kDw) {
+      // every die takes its share of each group, so that uneven groups spread
+      const int per = pl.nca * pl.nrb, share = (per * pl.splits + kXcd - 1) / kXcd;
+      g = j / share;
+      int l = xcd * share + j % share;
+      if (l >= per * pl.splits) return;
+      split = l / per;
+      l -= split * per;
+      group_rows(p.off, g, p.rows, lo, hi);
+      const int band = l / (pl.nrb * 4), rem = l - band * pl.nrb * 4, w = min(4, pl.nca - 4 * band);
+      r0 = rem / w * TB;
+      c0 = (4 * band + rem % w) * TA;
+      nr = min(TB, p.N - r0);
+      nred = hi - lo;
+      out0 = ((size_t)g * p.N + r0) * p.K + c0;
     } else {
-      stage_mc(sa, static_cast<const uint16_t*>(p.a) + (size_t)lo * p.K + c0, p.K, cols - c0, e0);
-      stage_mc(sb, static_cast<const uint16_t*>(p.b) + (size_t)lo * p.N + r0, p.N, nr, e0);
+      const int tiles = count_tiles<TB>(p.off, p.groups, p.rows) * pl.nca;
+      const int items = tiles * pl.splits, share = (items + kXcd - 1) / kXcd;
+      const int item = xcd * share + j;
+      if (j >= share || item >= items) return;
+      split = item / tiles;
+      const int l0 = item - split * tiles;
+      int t;
+      find_tile<TB>(p.off, p.groups, p.rows, l0 / pl.nca, g, t);
+      group_rows(p.off, g, p.rows, lo, hi);
+      const int nrb = (hi - lo + TB - 1) / TB, l = t * pl.nca + l0 % pl.nca;
+      const int band = l / (nrb * 4), rem = l - band * nrb * 4, w = min(4, pl.nca - 4 * band);
+      r0 = lo + rem / w * TB;
+      c0 = (4 * band + rem % w) * TA;
+      nr = min(TB, hi - r0);
+      nred = OP == kFwd ? p.K : p.N;
+      out0 = (size_t)r0 * cols + c0;
     }
-    __syncthreads();
-    v4i a[2][2], b[2][2];
+  }
+  const int nst = (nred + C::RE - 1) / C::RE;
+  int s_lo, s_n;  // the block's stages
+  {
+    const int sps = OP == kDw ? (nst + pl.splits - 1) / pl.splits : pl.sps;
+    s_lo = min(nst, split * sps);
+    s_n = min(sps, nst - s_lo);
+  }
+
+  // ---- DMA.  A contiguous-reduction operand is staged as rows of 128 bytes,
+  // 8 rows per instruction; a transposed one as reduction rows of T columns.
+  // The 16-byte pieces of a row are permuted so that the reads below spread
+  // over the LDS banks.
+  const int ldr = OP == kFwd ? p.K : p.N;  // row length of a contiguous-reduction operand
+  const uint8_t *abase, *bbase;
+  uint32_t alim = 0, blim = 0;
+  const uint8_t* wslab = static_cast<const uint8_t*>(p.a) + (OP == kDw ? 0 : (size_t)g * p.N * p.K * ES);
+  if (OP == kFwd) {
+    abase = wslab + (size_t)c0 * p.K * ES;
+    alim = (uint32_t)min(TA, p.N - c0) * (uint32_t)(p.K * ES);
+  } else if (OP == kDx) {
+    abase = wslab + (size_t)c0 * 2;
+  } else {
+    abase = static_cast<const uint8_t*>(p.a) + ((size_t)lo * p.K + c0) * 2;
+  }
+  if (OP == kDw) {
+    bbase = static_cast<const uint8_t*>(p.b) + ((size_t)lo * p.N + r0) * 2;
+  } else {
+    bbase = static_cast<const uint8_t*>(p.b) + (size_t)r0 * ldr * ES;
+    blim = (uint32_t)nr * (uint32_t)(ldr * ES);
+  }
+  uint32_t avo[C::NA], bvo[C::NB];
+  auto offs_kc = [&](uint32_t* vo, int n, bool perm) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int m = 0; m < n; ++m) {
+      const int row = 8 * (wave + W * m) + (lane >> 3);
+      const int f = perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7;
+      vo[m] = (uint32_t)row * (uint32_t)(ldr * ES) + 16u * (uint32_t)((lane & 7) ^ f);
+    }
+  };
+  auto offs_mc = [&](uint32_t* vo, int n, int T, int ld, int ncol) {
+    const int PR = T / 8, RPI = 64 / PR;  // pieces per row, rows per instruction
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[i][h] = *reinterpret_cast<const v4i*>(sa + (wa * 32 + i * 16 + l16) * kPitch + h * 64 + q * 16);
-        b[i][h] = *reinterpret_cast<const v4i*>(sb + (wb * 32 + i * 16 + l16) * kPitch + h * 64 + q * 16);
+    for (int m = 0; m < n; ++m) {
+      const int row = (wave + W * m) * RPI + lane / PR;
+      const int f = (row & 3) | ((row >> 1) & 4);
+      const int pc = (lane % PR) ^ ((2 * f) & (PR - 1));
+      vo[m] = 8 * pc < ncol ? ((uint32_t)row * (uint32_t)ld + 8u * pc) * 2u : kOob;
+    }
+  };
+  if (C::AT) offs_mc(avo, C::NA, TA, p.K, cols - c0);
+  else offs_kc(avo, C::NA, true);
+  if (C::BT) offs_mc(bvo, C::NB, TB, p.N, nr);
+  else offs_kc(bvo, C::NB, false);
+
+  // fp8 scales: one dword per lane and stage; waves [0, TB / 64): the rows',
+  // the last wave: the weights', per 128 columns of the tile
+  const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
+  const float* scp = nullptr;
+  uint32_t sclim = 0, scvo = kOob;
+  if constexpr (IN == kFP8) {
+    if (wave < (TB + 63) / 64) {
+      scp = p.bs + (size_t)r0 * nkb;
+      sclim = (uint32_t)(nr * nkb) * 4u;
+      if (wave * 64 + lane < TB) scvo = (uint32_t)((wave * 64 + lane) * nkb) * 4u;
+    } else if (wave == W - 1) {
+      scp = p.as + ((size_t)g * nnb + c0 / 128) * nkb;
+      sclim = (uint32_t)((nnb - c0 / 128) * nkb) * 4u;
+      if (lane < (TA + 127) / 128) scvo = (uint32_t)(lane * nkb) * 4u;
+    }
+    // wave-uniform by construction; said so, for the buffer descriptor
+    const uint64_t a = (uint64_t)(uintptr_t)scp;
+    scp = reinterpret_cast<const float*>((uintptr_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
+                                                     (uint32_t)__builtin_amdgcn_readfirstlane((int)a)));
+    sclim = (uint32_t)__builtin_amdgcn_readfirstlane((int)sclim);
+  }
+
+  // stage st of the reduction into a ring slot
+  auto dma = [&](lds_u8* wr, int st) __attribute__((always_inline)) {
+    const bool tail = (st + 1) * 128 > ldr * ES;  // the row ends inside the stage
+    const uint32_t so = (uint32_t)st * 128u;
+    auto kc = [&](const uint8_t* base, uint32_t lim, const uint32_t* vo, int n, bool perm, lds_u8* dst) {
+      const rsrc_t r = make_rsrc(base, lim);
+#pragma unroll
+      for (int m = 0; m < n; ++m) {
+        uint32_t v = vo[m];
+        if (tail) {
+          const int row = 8 * (wave + W * m) + (lane >> 3);
+          const int f = perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7;
+          if (so + 16u * (uint32_t)((lane & 7) ^ f) >= (uint32_t)(ldr * ES)) v = kOob;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(dst + (wave + W * m) * 1024), 16, v, so, 0, 0);
+      }
+    };
+    auto mc = [&](const uint8_t* base, int ld, int col0, const uint32_t* vo, int n, lds_u8* dst) {
+      const int rows = min(C::RE, nred - st * C::RE);
+      const rsrc_t r = make_rsrc(base + (size_t)st * C::RE * ld * 2, (uint32_t)(rows * ld - col0) * 2u);
+#pragma unroll
+      for (int m = 0; m < n; ++m)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(dst + (wave + W * m) * 1024), 16, vo[m], 0, 0, 0);
+    };
+    if (C::AT) mc(abase, p.K, c0, avo, C::NA, wr);
+    else kc(abase, alim, avo, C::NA, true, wr);
+    if (C::BT) mc(bbase, p.N, r0, bvo, C::NB, wr + TA * 128);
+    else kc(bbase, blim, bvo, C::NB, false, wr + TA * 128);
+    if constexpr (IN == kFP8)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(scp, sclim), (lds_void)(wr + (TA + TB) * 128 + wave * 256), 4,
+                                               scvo, (uint32_t)st * 4u, 0, 0);
+  };
+
+  // ---- LDS reads.  Contiguous reduction: lane (l16, q) of a tile reads pieces
+  // q and q + 4 of its row.  A's tiles interleave their columns (tile i, row
+  // 4 u + e is column PGS u + 4 i + e), so that a lane ends with PGS
+  // consecutive columns.  Transposed: a 16-lane group reads four reduction
+  // rows of 16 columns, each lane getting one column's four values.
+  const int fa = C::AT ? (l16 >> 2) | ((q & 1) << 2) : (l16 & 3) | (((l16 >> 2) & 1) << 2);
+  const int fb = C::BT ? (l16 >> 2) | ((q & 1) << 2) : l16 & 7;
+  const uint32_t ra = (uint32_t)(wa * TI * 16 + C::PGS * (l16 >> 2) + (l16 & 3)) * 128;
+  const uint32_t rb = (uint32_t)(TA * 128 + (wb * TJ * 16 + l16) * 128);
+  auto ld_kc = [&](const lds_u8* rd, uint32_t row, int kk, int f) {
+    return *reinterpret_cast<const lds_v4i*>(rd + row + (((4 * kk + q) ^ f) * 16));
+  };
+  auto ld_mc = [&](const lds_u8* rd, int T, int tile, int kk, int f) {
+    const int row = 32 * kk + 8 * q + (l16 >> 2);
+    const lds_u8* a = rd + row * T * 2 + (((tile ^ f) & (T / 16 - 1)) | (tile & ~(T / 16 - 1))) * 32 + (l16 & 3) * 8;
+    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a);
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(a + 4 * T * 2));
+    typedef short v8s __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(v4i, (v8s)__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto lda = [&](const lds_u8* rd, int i, int kk) {
+    if constexpr (C::AT) return ld_mc(rd, TA, wa * TI + i, kk, fa);
+    else return ld_kc(rd, ra + (uint32_t)((i / C::PG) * C::PG * 16 + (i % C::PG) * 4) * 128, kk, fa);
+  };
+  auto ldb = [&](const lds_u8* rd, int j, int kk) {
+    if constexpr (C::BT) return ld_mc(rd + TA * 128, TB, wb * TJ + j, kk, fb);
+    else return ld_kc(rd, rb + (uint32_t)(j * 16) * 128, kk, fb);
+  };
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const lds_u8* rd) __attribute__((always_inline)) {
+    if constexpr (IN == kFP8) {
+      const lds_f32* sc = reinterpret_cast<const lds_f32*>(rd + (TA + TB) * 128);
+      const float wsc = sc[(W - 1) * 64 + (wa * TI * 16) / 128];
+      float s[TJ];
+      v8i b[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        s[j] = sc[wb * TJ * 16 + 16 * j + l16] * wsc;
+        const v4i b0 = ldb(rd, j, 0), b1 = ldb(rd, j, 1);
+        b[j] = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
       }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float s = 0.0f;
-      if constexpr (IN == kFP8) {
-        const int row = wb * 32 + j * 16 + l16;
-        const float xs = row < nr ? p.bs[(size_t)(r0 + row) * nkb + e0 / 128] : 0.0f;
-        s = xs * p.as[((size_t)g * nnb + c0 / 128) * nkb + e0 / 128];  // the tile lies in one block of 128 columns
+      for (int i = 0; i < TI; ++i) {
+        const v4i a0 = lda(rd, i, 0), a1 = lda(rd, i, 1);
+        const v8i a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+        v4f d[TJ];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) d[j] = mfma8(a, b[j], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (IN == kFP8) {
-          v8i av, bv;
+      for (int kk = 0; kk < 2; ++kk) {
+        v4i b[TJ];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) av[d] = a[i][0][d], av[4 + d] = a[i][1][d], bv[d] = b[j][0][d], bv[4 + d] = b[j][1][d];
-          const v4f d = mfma8(av, bv, v4f{0.f, 0.f, 0.f, 0.f});
+        for (int j = 0; j < TJ; ++j) b[j] = ldb(rd, j, kk);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
-        } else {
-          acc[i][j] = mfma16<IN>(a[i][0], b[j][0], acc[i][j]);
-          acc[i][j] = mfma16<IN>(a[i][1], b[j][1], acc[i][j]);
+        for (int i = 0; i < TI; ++i) {
+          const v4i a = lda(rd, i, kk);
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j] = mfma16<IN>(a, b[j], acc[i][j]);
         }
       }
     }
-    __syncthreads();
+  };
+
+  // One call site for every DMA and every read: stage s + PRE is fetched while
+  // stage s is computed.
+  auto step = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, int s) __attribute__((always_inline)) {
+    if (s + PRE < s_n) dma(wr, s_lo + s + PRE);
+    if (s >= 0) compute(rd);
+  };
+  lds_u8* const ring0 = (lds_u8*)ring;
+  int wslot = 0, rslot = 0;
+  for (int s = -PRE; s < s_n; ++s) {
+    if (s >= 0) {
+      // this wave's part of stage s has landed (the PRE - 1 younger stages may
+      // be in flight) and its reads of stage s - 1 are done; then the barrier
+      // says the same of every wave
+      if (s + PRE - 1 < s_n) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((PRE - 1) * C::NI) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+    step(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, s);
+    wslot = wslot == NS - 1 ? 0 : wslot + 1;
+    if (s >= 0) rslot = rslot == NS - 1 ? 0 : rslot + 1;
   }
+
+  // ---- the tile's values, rounded once to the output type
+  auto write = [&](auto outc, void* out) {
+    constexpr int OUT = decltype(outc)::value;
+    using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
+    constexpr int V = C::AT ? 4 : C::PGS;  // consecutive columns of a lane
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < TJ; ++j) {
+      const int r = wb * TJ * 16 + 16 * j + l16;
+      if (r >= nr) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int u = 0; u < TI * 4 / V; ++u) {
+        const int c = wa * TI * 16 + (C::AT ? 16 * u + 4 * q : C::PG * 16 * u + V * q);
+        O v[V];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = wa * 32 + i * 16 + 4 * q + e, r = wb * 32 + j * 16 + l16;
-        if (r < nr && c0 + c < cols) store1<OUT>(p.out, out0 + (size_t)r * cols + c, acc[i][j][e]);
+        for (int i = 0; i < V / 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * i + e] = (O)acc[u * (V / 4) + i][j][e];
+        O* o = static_cast<O*>(out) + out0 + (size_t)r * cols + c;
+        if (c0 + c + V <= cols) {
+          __builtin_memcpy(o, v, sizeof v);  // rows start at any multiple of the type's size
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (c0 + c + e < cols) o[e] = v[e];
+        }
       }
+    }
+  };
+  if (pl.splits > 1) {
+    const size_t total = (size_t)(OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;
+    write(std::integral_constant<int, kF32>{}, static_cast<float*>(p.part) + split * total);
+  } else if (pl.out_type == kF32) {
+    write(std::integral_constant<int, kF32>{}, p.out);
+  } else if (IN == kF16 || (IN == kFP8 && pl.out_type == kF16)) {
+    write(std::integral_constant<int, kF16>{}, p.out);
+  } else {
+    write(std::integral_constant<int, kBF16>{}, p.out);
+  }
 }
 
-template <int IN, int OP, int OUT>
-hipError_t run_linear(const LinearArgs& p, hipStream_t st) {
-  const unsigned ca = (unsigned)(((OP == kFwd ? p.N : p.K) + kTile - 1) / kTile);
-  // row tiles: every group adds at most one partial tile
-  const unsigned rb = OP == kDw ? (unsigned)((p.N + kTile - 1) / kTile)
-                                : (unsigned)(p.rows / kTile + (p.rows < p.groups ? p.rows : p.groups));
-  if (OP != kDw && rb == 0) return hipSuccess;
-  k_linear<IN, OP, OUT><<<dim3(ca, rb, OP == kDw ? p.groups : 1), 256, 0, st>>>(p);
+// out = sum of the splits' partial sums, in split order.  kFwd, kDx: rows in
+// no group have none and are left alone.
+template <int OUT>
+__global__ void __launch_bounds__(256) k_linear_join(LinearArgs p, size_t total, int cols, int splits, bool rows_out) {
+  using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
+  size_t i0 = 0, i1 = total;
+  if (rows_out && p.off) {
+    i0 = (size_t)min(max(p.off[0], 0), p.rows) * cols;
+    i1 = (size_t)min(max(p.off[p.groups], 0), p.rows) * cols;
+  }
+  const bool quad = cols % 4 == 0;  // 4 values a thread: every row and partial starts 16-byte aligned
+  const size_t step = (size_t)gridDim.x * 256, t = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const float* part = static_cast<const float*>(p.part);
+  O* out = static_cast<O*>(p.out);
+  if (quad) {
+    for (size_t i = i0 + 4 * t; i < i1; i += 4 * step) {
+      v4f s = *reinterpret_cast<const v4f*>(part + i);
+      for (int z = 1; z < splits; ++z) s += *reinterpret_cast<const v4f*>(part + z * total + i);
+      O v[4] = {(O)s[0], (O)s[1], (O)s[2], (O)s[3]};
+      __builtin_memcpy(out + i, v, sizeof v);
+    }
+  } else {
+    for (size_t i = i0 + t; i < i1; i += step) {
+      float s = part[i];
+      for (int z = 1; z < splits; ++z) s += part[z * total + i];
+      out[i] = (O)s;
+    }
+  }
+}
+
+constexpr int kMaxSplits = 16;
+constexpr int kCus = 256;
+
+// Tile shapes, largest first (columns x rows of the output): index, TA, TB
+constexpr int kShapes = 4;
+constexpr int kTA[kShapes] = {256, 256, 128, 128}, kTB[kShapes] = {256, 128, 64, 32};
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+struct Choice {
+  int shape;
+  Plan plan;
+};
+
+Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
+  const int es = in_type == kFP8 ? 1 : 2, re = 128 / es;
+  const int cols = op == kFwd ? N : K;
+  const int avg = op == kDw ? N : ceil_div(rows, groups);
+  Choice c{};
+  auto tiles = [&](int s) {
+    const long nca = ceil_div(cols, kTA[s]);
+    const long nrb = op == kDw ? (long)ceil_div(N, kTB[s]) * groups : rows / kTB[s] + (rows < groups ? rows : groups);
+    return nca * (nrb > 0 ? nrb : 1);
+  };
+  int s = avg > 128 ? 0 : (avg > 64 ? 1 : (avg > 32 ? 2 : 3));
+  while (s < 2 && tiles(s) < kCus) ++s;
+  c.shape = s;
+  c.plan.nca = ceil_div(cols, kTA[s]);
+  c.plan.nrb = op == kDw ? ceil_div(N, kTB[s]) : (int)(tiles(s) / c.plan.nca);
+  // split the reduction while the tiles leave compute units idle, at least
+  // four stages a piece
+  const int nst = ceil_div(op == kFwd ? K : (op == kDx ? N : ceil_div(rows, groups)), re);
+  int split = (int)(kCus / tiles(s));
+  split = split < nst / 4 ? split : nst / 4;
+  split = split < kMaxSplits ? split : kMaxSplits;
+  if (split < 1) split = 1;
+  c.plan.sps = ceil_div(nst > 0 ? nst : 1, split);
+  c.plan.splits = op == kDw ? split : ceil_div(nst > 0 ? nst : 1, c.plan.sps);
+  return c;
+}
+
+size_t part_bytes(int op, int in_type, int rows, int N, int K, int groups) {
+  const Choice c = choose(op, in_type, rows, N, K, groups);
+  if (c.plan.splits == 1) return 0;
+  const size_t out = op == kFwd ? (size_t)rows * N : (op == kDx ? (size_t)rows * K : (size_t)groups * N * K);
+  return out * c.plan.splits * sizeof(float);
+}
+
+template <class C>
+hipError_t run_shape(const LinearArgs& p, const Plan& pl, hipStream_t st) {
+  long blocks;
+  if (C::OP == kDw) blocks = (long)p.groups * (ceil_div(pl.nca * pl.nrb * pl.splits, kXcd) * kXcd);
+  else blocks = (long)ceil_div(pl.nca * pl.nrb * pl.splits, kXcd) * kXcd;
+  k_linear<C><<<dim3((unsigned)blocks), C::W * 64, 0, st>>>(p, pl);
   return hipGetLastError();
 }
 
 template <int IN, int OP>
-hipError_t run_out(int out_type, const LinearArgs& p, hipStream_t st) {
-  if (out_type == kBF16) return run_linear<IN, OP, kBF16>(p, st);
-  if (out_type == kF16) return run_linear<IN, OP, kF16>(p, st);
-  return run_linear<IN, OP, kF32>(p, st);
+hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
+  Choice c = choose(OP, IN, p.rows, p.N, p.K, p.groups);
+  c.plan.out_type = out_type;
+  p.part = ws;
+  hipError_t e;
+  if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 2, 1>>(p, c.plan, st);
+  else if (c.shape == 1) e = run_shape<Shape<IN, OP, 256, 128, 4, 2, 3, 1>>(p, c.plan, st);
+  else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 3, 2>>(p, c.plan, st);
+  else e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 3, 2>>(p, c.plan, st);
+  if (e != hipSuccess || c.plan.splits == 1) return e;
+  const int cols = OP == kFwd ? p.N : p.K;
+  const size_t total = (OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;
+  const size_t want = (cols % 4 == 0 ? total / 4 : total) / 256 + 1;
+  const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
+  if (out_type == kBF16) k_linear_join<kBF16><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
+  else if (out_type == kF16) k_linear_join<kF16><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
+  else k_linear_join<kF32><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
+  return hipGetLastError();
 }
 
 template <int IN>
-hipError_t run_op(int op, int out_type, const LinearArgs& p, hipStream_t st) {
-  if (op == kFwd) return run_out<IN, kFwd>(out_type, p, st);
-  if (op == kDx) return run_out<IN, kDx>(out_type, p, st);
-  return run_out<IN, kDw>(out_type, p, st);
+hipError_t run_in(int op, int out_type, const LinearArgs& p, void* ws, hipStream_t st) {
+  if (op == kFwd) return run_op<IN, kFwd>(out_type, p, ws, st);
+  if (op == kDx) return run_op<IN, kDx>(out_type, p, ws, st);
+  return run_op<IN, kDw>(out_type, p, ws, st);
 }
 
 }  // namespace
 
-size_t linear_workspace(int, int, int, int, int) { return 0; }
+size_t linear_workspace(int rows, int N, int K, int groups, int in_type) {
+  size_t n = part_bytes(kFwd, in_type, rows, N, K, groups);
+  if (in_type != kFP8)
+    for (int op = kDx; op <= kDw; ++op) {
+      const size_t m = part_bytes(op, in_type, rows, N, K, groups);
+      n = m > n ? m : n;
+    }
+  return n;
+}
 
-hipError_t launch_linear(int op, int in_type, int out_type, const LinearArgs& p, void*, hipStream_t st) {
-  if (in_type == kFP8) return run_out<kFP8, kFwd>(out_type, p, st);
-  return in_type == kBF16 ? run_op<kBF16>(op, out_type, p, st) : run_op<kF16>(op, out_type, p, st);
+hipError_t launch_linear(int op, int in_type, int out_type, const LinearArgs& p, void* ws, hipStream_t st) {
+  if (in_type == kFP8) return run_op<kFP8, kFwd>(out_type, p, ws, st);
+  return in_type == kBF16 ? run_in<kBF16>(op, out_type, p, ws, st) : run_in<kF16>(op, out_type, p, ws, st);
 }
 
 }  // namespace moe

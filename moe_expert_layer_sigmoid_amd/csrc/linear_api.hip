@@ -83,7 +83,7 @@ int moe_fp8_linear(const moe_linear_t* d, const uint8_t* xq, const float* xs, co
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_call(d, offsets, workspace, workspace_bytes))) return rc;
   if (d->rows == 0) return MOE_OK;
-  const LinearArgs p{w, xq, ws, xs, offsets, y, d->rows, d->N, d->K, d->groups};
+  const LinearArgs p{w, xq, ws, xs, offsets, y, d->rows, d->N, d->K, d->groups, nullptr};
   return hip_status(launch_linear(kFwd, d->in_type, d->out_type, p, workspace, (hipStream_t)stream));
 }
 
@@ -95,7 +95,7 @@ int moe_grouped_linear(const moe_linear_t* d, const void* x, const void* w, cons
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_call(d, offsets, workspace, workspace_bytes))) return rc;
   if (d->rows == 0) return MOE_OK;
-  const LinearArgs p{w, x, nullptr, nullptr, offsets, y, d->rows, d->N, d->K, d->groups};
+  const LinearArgs p{w, x, nullptr, nullptr, offsets, y, d->rows, d->N, d->K, d->groups, nullptr};
   return hip_status(launch_linear(kFwd, d->in_type, d->out_type, p, workspace, (hipStream_t)stream));
 }
 
@@ -107,7 +107,7 @@ int moe_grouped_linear_dx(const moe_linear_t* d, const void* dy, const void* w, 
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_call(d, offsets, workspace, workspace_bytes))) return rc;
   if (d->rows == 0) return MOE_OK;
-  const LinearArgs p{w, dy, nullptr, nullptr, offsets, dx, d->rows, d->N, d->K, d->groups};
+  const LinearArgs p{w, dy, nullptr, nullptr, offsets, dx, d->rows, d->N, d->K, d->groups, nullptr};
   return hip_status(launch_linear(kDx, d->in_type, d->out_type, p, workspace, (hipStream_t)stream));
 }
 
@@ -118,7 +118,7 @@ int moe_grouped_linear_dw(const moe_linear_t* d, const void* dy, const void* x, 
   if (d->in_type == MOE_TYPE_FP8 || d->N % 8 || !rows_ok(dy, d->rows) || !rows_ok(x, d->rows) || !dev_ok(dw))
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_call(d, offsets, workspace, workspace_bytes))) return rc;
-  const LinearArgs p{x, dy, nullptr, nullptr, offsets, dw, d->rows, d->N, d->K, d->groups};
+  const LinearArgs p{x, dy, nullptr, nullptr, offsets, dw, d->rows, d->N, d->K, d->groups, nullptr};
   return hip_status(launch_linear(kDw, d->in_type, d->out_type, p, workspace, (hipStream_t)stream));
 }
 

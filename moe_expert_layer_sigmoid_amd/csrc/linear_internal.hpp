@@ -24,6 +24,7 @@ struct LinearArgs {
   const int32_t* off;  // [groups + 1], or nullptr: one group of all rows
   void* out;
   int rows, N, K, groups;
+  void* part;          // workspace: f32 partial sums of a split reduction
 };
 
 size_t linear_workspace(int rows, int N, int K, int groups, int in_type);

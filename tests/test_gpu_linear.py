@@ -205,6 +205,48 @@ def test_fp8_linear_exact_on_small_integers():
         assert np.array_equal(_np(y), ref), (rows, N, K)
 
 
+# Sizes at which every output tile shape is the one chosen, with tiles that
+# end inside the matrices.
+LARGE = [(4500, 1, 4352, 144), (2100, 3, 4232, 272), (1100, 12, 2200, 208), (400, 12, 2200, 208), (150, 12, 2200, 336)]
+
+
+def _int16(rng, *s):
+    return torch.from_numpy(rng.integers(-3, 4, s).astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("rows,groups,N,K", LARGE)
+def test_large_tiles_exact_on_small_integers(rows, groups, N, K):
+    """Small integers: every sum is exact in f32, so every product is the
+    integer one, for every type."""
+    _say(f"[case] large rows={rows} groups={groups} N={N} K={K}")
+    rng = _rng(16, rows, groups, N, K)
+    x, w, dy = _int16(rng, rows, K), _int16(rng, groups, N, K), _int16(rng, rows, N)
+    off = _offsets(rng, rows, groups) if groups > 1 else None
+    do = _dev_off(off)
+    ref = [torch.zeros(rows, N, device="cuda"), torch.zeros(rows, K, device="cuda"), torch.zeros(groups, N, K, device="cuda")]
+    for g, (lo, hi) in enumerate(ol.spans(off, rows)):
+        ref[0][lo:hi] = (x[lo:hi].double() @ w[g].double().t()).float()
+        ref[1][lo:hi] = (dy[lo:hi].double() @ w[g].double()).float()
+        ref[2][g] = (dy[lo:hi].double().t() @ x[lo:hi].double()).float()
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    d8 = mx.Linear(rows, N, K, groups=groups, in_type="fp8", out_type="f32")
+    y = torch.full((rows, N), 0.5, device="cuda")
+    mx.moe_fp8_linear(d8, x.to(torch.float8_e4m3fn), one(rows, ol.blocks(K)), w.to(torch.float8_e4m3fn),
+                      one(groups, ol.blocks(N), ol.blocks(K)), y, mx.linear_workspace(d8), offsets=do)
+    assert torch.equal(y, ref[0])
+    for dt in ("bf16", "f16"):
+        d = mx.Linear(rows, N, K, groups=groups, in_type=dt, out_type="f32")
+        ws = mx.linear_workspace(d)
+        o = [torch.full_like(r, 0.5) for r in ref]
+        xt, wt, dyt = x.to(T[dt]), w.to(T[dt]), dy.to(T[dt])
+        mx.moe_grouped_linear(d, xt, wt, o[0], ws, offsets=do)
+        mx.moe_grouped_linear_dx(d, dyt, wt, o[1], ws, offsets=do)
+        mx.moe_grouped_linear_dw(d, dyt, xt, o[2], ws, offsets=do)
+        torch.cuda.synchronize()
+        for got, r, name in zip(o, ref, ("y", "dx", "dw")):
+            assert torch.equal(got, r), (dt, name)
+
+
 def test_fp8_linear_keeps_other_groups_and_rows_apart():
     """NaN codes and scales in one group's rows and weights reach that group's
     outputs alone; rows in no group are not written."""
