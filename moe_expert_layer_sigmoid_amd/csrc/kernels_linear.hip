@@ -125,6 +125,10 @@ struct Shape {
   static constexpr int kScale = IN == kFP8 ? W * 256 : 0;
   static constexpr int kSlot = (TA + TB) * 128 + kScale;
   static constexpr int PRE = NS - 1;
+  static constexpr int U = IN == kFP8 ? TI : 2 * TI;  // steps of a stage (below)
+  static constexpr int D = IN == kFP8 ? 2 : 3;        // steps that operands are read ahead
+  static constexpr int kLag = TJ == 1 ? 2 : 3;
+  static_assert(U % 4 == 0 && D < 4 && kLag < 4 && (IN != kFP8 || kLag <= (U - D) * TJ), "rings of four");
   static_assert(NA * W * 8 == TA && NB * W * 8 == TB && TI * WA * 16 == TA && TJ * WB * 16 == TB, "tile shape");
   static_assert(PRE * NI < 64, "vmcnt range");
   static_assert(IN != kFP8 || TB / 64 < W, "a wave for the weight scales");
@@ -141,6 +145,7 @@ struct Plan {
 
 template <class C>
 __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearArgs p, Plan pl) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the kernel's name alone, and not every device builtin type-checks there
   constexpr int TA = C::TA, TB = C::TB, TI = C::TI, TJ = C::TJ, W = C::W, ES = C::ES, NS = C::NS, PRE = C::PRE;
   constexpr int IN = C::IN, OP = C::OP;
   __shared__ __align__(1024) uint8_t ring[NS * C::kSlot];
@@ -221,29 +226,26 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     bbase = static_cast<const uint8_t*>(p.b) + (size_t)r0 * ldr * ES;
     blim = (uint32_t)nr * (uint32_t)(ldr * ES);
   }
-  uint32_t avo[C::NA], bvo[C::NB];
-  auto offs_kc = [&](uint32_t* vo, int n, bool perm) {
-#pragma unroll
-    for (int m = 0; m < n; ++m) {
-      const int row = 8 * (wave + W * m) + (lane >> 3);
-      const int f = perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7;
-      vo[m] = (uint32_t)row * (uint32_t)(ldr * ES) + 16u * (uint32_t)((lane & 7) ^ f);
-    }
+  // Lane offsets of an operand's first instruction; instruction m is a uniform
+  // distance further.  (Rows 32 apart permute their pieces alike.)
+  auto kc_row = [&]() { return 8 * wave + (lane >> 3); };
+  auto kc_piece = [&](bool perm) {
+    const int row = kc_row();
+    return (lane & 7) ^ (perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7);
   };
-  auto offs_mc = [&](uint32_t* vo, int n, int T, int ld, int ncol) {
+  auto mc_off = [&](int T, int ld, int ncol) {
     const int PR = T / 8, RPI = 64 / PR;  // pieces per row, rows per instruction
-#pragma unroll
-    for (int m = 0; m < n; ++m) {
-      const int row = (wave + W * m) * RPI + lane / PR;
-      const int f = (row & 3) | ((row >> 1) & 4);
-      const int pc = (lane % PR) ^ ((2 * f) & (PR - 1));
-      vo[m] = 8 * pc < ncol ? ((uint32_t)row * (uint32_t)ld + 8u * pc) * 2u : kOob;
-    }
+    const int row = wave * RPI + lane / PR;
+    const int f = (row & 3) | ((row >> 1) & 4);
+    const int pc = (lane % PR) ^ ((2 * f) & (PR - 1));
+    return 8 * pc < ncol ? ((uint32_t)row * (uint32_t)ld + 8u * pc) * 2u : kOob;
   };
-  if (C::AT) offs_mc(avo, C::NA, TA, p.K, cols - c0);
-  else offs_kc(avo, C::NA, true);
-  if (C::BT) offs_mc(bvo, C::NB, TB, p.N, nr);
-  else offs_kc(bvo, C::NB, false);
+  const uint32_t apc = 16u * (uint32_t)kc_piece(true), bpc = 16u * (uint32_t)kc_piece(false);
+  const uint32_t rowb = (uint32_t)(ldr * ES);
+  const uint32_t avo = C::AT ? mc_off(TA, p.K, cols - c0) : (uint32_t)kc_row() * rowb + apc;
+  const uint32_t bvo = C::BT ? mc_off(TB, p.N, nr) : (uint32_t)kc_row() * rowb + bpc;
+  const uint32_t astep = C::AT ? (uint32_t)(W * (512 / TA) * p.K * 2) : 8 * W * rowb;
+  const uint32_t bstep = C::BT ? (uint32_t)(W * (512 / TB) * p.N * 2) : 8 * W * rowb;
 
   // fp8 scales: one dword per lane and stage; waves [0, TB / 64): the rows',
   // the last wave: the weights', per 128 columns of the tile
@@ -267,37 +269,33 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     sclim = (uint32_t)__builtin_amdgcn_readfirstlane((int)sclim);
   }
 
-  // stage st of the reduction into a ring slot
-  auto dma = [&](lds_u8* wr, int st) __attribute__((always_inline)) {
-    const bool tail = (st + 1) * 128 > ldr * ES;  // the row ends inside the stage
-    const uint32_t so = (uint32_t)st * 128u;
-    auto kc = [&](const uint8_t* base, uint32_t lim, const uint32_t* vo, int n, bool perm, lds_u8* dst) {
-      const rsrc_t r = make_rsrc(base, lim);
-#pragma unroll
-      for (int m = 0; m < n; ++m) {
-        uint32_t v = vo[m];
-        if (tail) {
-          const int row = 8 * (wave + W * m) + (lane >> 3);
-          const int f = perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7;
-          if (so + 16u * (uint32_t)((lane & 7) ^ f) >= (uint32_t)(ldr * ES)) v = kOob;
-        }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(dst + (wave + W * m) * 1024), 16, v, so, 0, 0);
-      }
+  // DMA instruction m of stage st into a ring slot.  Stages past the end load
+  // nothing (their buffers have no bytes), so that every stage counts the
+  // same number of loads.
+  auto dma = [&](lds_u8* wr, int st, int m, bool live) __attribute__((always_inline)) {
+    auto kc = [&](const uint8_t* base, uint32_t lim, uint32_t vo, uint32_t pc, uint32_t step, int m, lds_u8* dst) {
+      const uint32_t so = (uint32_t)st * 128u;
+      const uint32_t v = so + pc < rowb ? vo : kOob;  // pieces past the row's end
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, live ? lim : 0u), (lds_void)(dst + (wave + W * m) * 1024), 16,
+                                               v + (uint32_t)m * step, so, 0, 0);
     };
-    auto mc = [&](const uint8_t* base, int ld, int col0, const uint32_t* vo, int n, lds_u8* dst) {
-      const int rows = min(C::RE, nred - st * C::RE);
-      const rsrc_t r = make_rsrc(base + (size_t)st * C::RE * ld * 2, (uint32_t)(rows * ld - col0) * 2u);
-#pragma unroll
-      for (int m = 0; m < n; ++m)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(dst + (wave + W * m) * 1024), 16, vo[m], 0, 0, 0);
+    auto mc = [&](const uint8_t* base, int ld, int col0, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
+      const int rows = live ? min(C::RE, nred - st * C::RE) : 0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          make_rsrc(base + (size_t)st * C::RE * ld * 2, rows > 0 ? (uint32_t)(rows * ld - col0) * 2u : 0u),
+          (lds_void)(dst + (wave + W * m) * 1024), 16, vo + (uint32_t)m * step, 0, 0, 0);
     };
-    if (C::AT) mc(abase, p.K, c0, avo, C::NA, wr);
-    else kc(abase, alim, avo, C::NA, true, wr);
-    if (C::BT) mc(bbase, p.N, r0, bvo, C::NB, wr + TA * 128);
-    else kc(bbase, blim, bvo, C::NB, false, wr + TA * 128);
-    if constexpr (IN == kFP8)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(scp, sclim), (lds_void)(wr + (TA + TB) * 128 + wave * 256), 4,
-                                               scvo, (uint32_t)st * 4u, 0, 0);
+    if (m < C::NA) {
+      if (C::AT) mc(abase, p.K, c0, avo, astep, m, wr);
+      else kc(abase, alim, avo, apc, astep, m, wr);
+    } else if (m < C::NA + C::NB) {
+      if (C::BT) mc(bbase, p.N, r0, bvo, bstep, m - C::NA, wr + TA * 128);
+      else kc(bbase, blim, bvo, bpc, bstep, m - C::NA, wr + TA * 128);
+    } else if constexpr (IN == kFP8) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(scp, live ? sclim : 0u),
+                                               (lds_void)(wr + (TA + TB) * 128 + wave * 256), 4, scvo, (uint32_t)st * 4u,
+                                               0, 0);
+    }
   };
 
   // ---- LDS reads.  Contiguous reduction: lane (l16, q) of a tile reads pieces
@@ -335,68 +333,127 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const lds_u8* rd) __attribute__((always_inline)) {
+  // ---- main loop.  A stage is U steps of one A tile against all of the wave's
+  // B tiles (fp8: whole 128 columns; 16-bit: half by half).  A's operands are
+  // read D steps ahead, and the last D steps of a stage run after the barrier
+  // that ends it, from registers, while the next stage's first operands are on
+  // their way: no wave stands at the start of a stage waiting for LDS.  The
+  // next DMA is issued in between, instruction by instruction.  fp8: a tile's
+  // product is scaled and added kLag products later, when it is long finished.
+  constexpr int U = C::U, D = C::D, kLag = C::kLag;
+  constexpr int KH = U / TI;  // halves of a stage
+  v8i a[IN == kFP8 ? 4 : 1], b[IN == kFP8 ? TJ : 1];
+  v4i ah[IN == kFP8 ? 1 : 4], bh[IN == kFP8 ? 1 : 2][TJ];
+  float sold[TJ], snew[TJ], wsc = 0.f;
+  v4f part[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (IN == kFP8) a[i] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+    else ah[i] = v4i{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    sold[j] = snew[j] = 0.f;
+    if constexpr (IN == kFP8) b[j] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+    else bh[0][j] = bh[1][j] = v4i{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[i] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto join8 = [](v4i x, v4i y) -> v8i { return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7); };
+  auto read_a = [&](const lds_u8* rd, int u) __attribute__((always_inline)) {
+    if constexpr (IN == kFP8) a[u % 4] = join8(lda(rd, u, 0), lda(rd, u, 1));
+    else ah[u % 4] = lda(rd, u % TI, u / TI);
+  };
+  // fp8: adds product n (counted through the stage; negative: of the stage before)
+  auto promote = [&](int n) __attribute__((always_inline)) {
+    const int i = ((n + U * TJ) / TJ) % U, j = (n + U * TJ) % TJ;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[i][j][e] = fmaf(part[(n + 4) % 4][e], n + kLag >= (U - D) * TJ || n < 0 ? sold[j] : snew[j], acc[i][j][e]);
+  };
+  auto step = [&](int u, const lds_u8* rd, bool read_next) __attribute__((always_inline)) {
+    // reads for the steps ahead (rd: this stage for u < U - D, else the next)
+    if (read_next) read_a(rd, (u + D) % U);
     if constexpr (IN == kFP8) {
-      const lds_f32* sc = reinterpret_cast<const lds_f32*>(rd + (TA + TB) * 128);
-      const float wsc = sc[(W - 1) * 64 + (wa * TI * 16) / 128];
-      float s[TJ];
-      v8i b[TJ];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        s[j] = sc[wb * TJ * 16 + 16 * j + l16] * wsc;
-        const v4i b0 = ldb(rd, j, 0), b1 = ldb(rd, j, 1);
-        b[j] = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const v4i a0 = lda(rd, i, 0), a1 = lda(rd, i, 1);
-        const v8i a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-        v4f d[TJ];
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) d[j] = mfma8(a, b[j], v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s[j], acc[i][j][e]);
+        part[(u * TJ + j) % 4] = mfma8(a[u % 4], b[j], v4f{0.f, 0.f, 0.f, 0.f});
+        promote(u * TJ + j - kLag);
+        if (read_next && u == U - 1) b[j] = join8(ldb(rd, j, 0), ldb(rd, j, 1));
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
+      if (read_next) {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        v4i b[TJ];
+        for (int h = 0; h < KH; ++h)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) b[j] = ldb(rd, j, kk);
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-          const v4i a = lda(rd, i, kk);
-#pragma unroll
-          for (int j = 0; j < TJ; ++j) acc[i][j] = mfma16<IN>(a, b[j], acc[i][j]);
-        }
+          for (int j = 0; j < TJ; ++j)  // B's next half, spread over the D steps before it
+            if ((u + D - (j * D) / TJ) % U == h * TI) bh[h][j] = ldb(rd, j, h);
       }
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[u % TI][j] = mfma16<IN>(ah[u % 4], bh[u / TI][j], acc[u % TI][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // One call site for every DMA and every read: stage s + PRE is fetched while
-  // stage s is computed.
-  auto step = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, int s) __attribute__((always_inline)) {
-    if (s + PRE < s_n) dma(wr, s_lo + s + PRE);
-    if (s >= 0) compute(rd);
+  // From one barrier to the next: stage s's slot rd is complete, wr is free.
+  auto body = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, int s) __attribute__((always_inline)) {
+    const int st = s_lo + s + PRE;
+    const bool live = s + PRE < s_n;
+    if (s < 0) {
+#pragma unroll
+      for (int m = 0; m < C::NI; ++m) dma(wr, st, m, live);
+      return;
+    }
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+#pragma unroll
+      for (int m = 0; m < C::NI; ++m)
+        if (m * U / C::NI == v) dma(wr, st, m, live);
+      if constexpr (IN == kFP8) {
+        const lds_f32* sc = reinterpret_cast<const lds_f32*>(rd + (TA + TB) * 128);
+        if (v == 0) {
+          wsc = sc[(W - 1) * 64 + (wa * TI * 16) / 128];
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) {
+            sold[j] = snew[j];
+            snew[j] = sc[wb * TJ * 16 + 16 * j + l16];
+          }
+        }
+        if (v == D) {
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) snew[j] *= wsc;
+        }
+      }
+      step((v + U - D) % U, rd, true);
+    }
   };
   lds_u8* const ring0 = (lds_u8*)ring;
   int wslot = 0, rslot = 0;
   for (int s = -PRE; s < s_n; ++s) {
     if (s >= 0) {
-      // this wave's part of stage s has landed (the PRE - 1 younger stages may
-      // be in flight) and its reads of stage s - 1 are done; then the barrier
+      // this wave's part of stage s has landed (PRE - 1 younger stages may be
+      // in flight) and its reads of stage s - 1 are done; then the barrier
       // says the same of every wave
-      if (s + PRE - 1 < s_n) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((PRE - 1) * C::NI) : "memory");
-      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((PRE - 1) * C::NI) : "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
-    step(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, s);
+    body(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, s);
     wslot = wslot == NS - 1 ? 0 : wslot + 1;
     if (s >= 0) rslot = rslot == NS - 1 ? 0 : rslot + 1;
   }
+  // the last stage's last steps
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) sold[j] = snew[j];
+#pragma unroll
+  for (int u = U - D; u < U; ++u) step(u, nullptr, false);
+  if constexpr (IN == kFP8) {
+#pragma unroll
+    for (int n = U * TJ - kLag; n < U * TJ; ++n) promote(n);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
 
   // ---- the tile's values, rounded once to the output type
   auto write = [&](auto outc, void* out) {
@@ -436,6 +493,7 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
   } else {
     write(std::integral_constant<int, kBF16>{}, p.out);
   }
+#endif
 }
 
 // out = sum of the splits' partial sums, in split order.  kFwd, kDx: rows in
