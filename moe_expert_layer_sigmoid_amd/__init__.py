@@ -61,6 +61,7 @@ class Dims(ctypes.Structure):
 
 TYPES = {"bf16": 0, "f16": 1, "f32": 2, "fp8": 3}   # moe_type_t
 _TORCH_TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn)
+_QUANT_TYPES = {t: i for i, t in enumerate(_TORCH_TYPES[:3])}
 
 
 class Linear(ctypes.Structure):
@@ -530,28 +531,42 @@ def linear_workspace(d: Linear, device="cuda") -> torch.Tensor:
     return torch.empty(max(moe_linear_workspace_bytes(d), 256), dtype=u8, device=device)
 
 
-def _addr(t: torch.Tensor, name: str, dtype, numel_min: int, dev) -> int:
-    """_ptr for the linear operators, whose smallest calls take a few us: the
-    address as an int, and every tensor on the same device as the first."""
+# The smallest linear calls take a few us on the GPU, so their host side is
+# kept short: one pass of checks per tensor, addresses as plain ints, the
+# current stream without a Stream object (measured: 10.0 -> HOSTUS us a call).
+
+def _addr(t: torch.Tensor, name: str, dtype, numel_min: int, dev: int) -> int:
+    """The address of a tensor that fits; _refuse says why one does not."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and t.numel() >= numel_min and dev >= 0):
+        return t.data_ptr()
+    return _refuse(t, name, dtype, numel_min, dev)
+
+
+def _refuse(t, name, dtype, numel_min, dev) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype and not (dtype is torch.float8_e4m3fn and t.dtype is u8):
+    if dtype is torch.float8_e4m3fn and t.dtype is u8:   # codes as bytes
+        return _addr(t, name, u8, numel_min, dev)
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != dev or dev.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}, must be on one device (the first tensor is on {dev})")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on cuda:{dev}" if dev >= 0 else
+                         f"{name}: on {t.device}, another tensor on the host")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.numel() < numel_min:
-        raise ValueError(f"{name}: {t.numel()} elements, need at least {numel_min}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {t.numel()} elements, need at least {numel_min}")
 
 
-def _launch(fn: str, dev: torch.device, stream, *args) -> None:
+def _launch(fn: str, dev: int, stream, *args) -> None:
     """Call ``fn`` on the tensors' device, on its current stream by default."""
-    if dev.index != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _launch(fn, dev, stream, *args)
-    rc = getattr(lib(), fn)(*args, _stream(stream))
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    rc = getattr(lib(), fn)(*args, st)
     if rc != MOE_OK:
         raise MoeError(fn, rc)
 
@@ -564,17 +579,18 @@ def _fp8_quant(fn: str, x, q, qs, parts: int, stream) -> None:
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x: expected a torch.Tensor of two dimensions")
     rows, K = x.shape[0], x.shape[1] // parts
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("x: must be a device tensor")
-    if x.dtype not in _TORCH_TYPES[:3]:
+    t = _QUANT_TYPES.get(x.dtype)
+    if t is None:
         raise TypeError(f"x: dtype {x.dtype}, expected bfloat16, float16 or float32")
     if x.shape[1] != parts * K or (x.stride(1) != 1 and x.numel()):
         raise ValueError("x: the columns must be contiguous" + (" and even in number" if parts == 2 else ""))
     ldx = x.stride(0) if rows > 1 else parts * K
     if ldx < parts * K:
         raise ValueError("x: the rows must not overlap")
-    dev = x.device
-    _launch(fn, dev, stream, rows, K, _TORCH_TYPES.index(x.dtype), x.data_ptr(), ldx,
+    dev = x.get_device()
+    _launch(fn, dev, stream, rows, K, t, x.data_ptr(), ldx,
             _addr(q, "q", torch.float8_e4m3fn, rows * K, dev), _addr(qs, "qs", f32, rows * _blocks(K), dev))
 
 
@@ -603,7 +619,7 @@ def moe_fp8_linear(d: Linear, xq, xs, w, ws, y, scratch, offsets=None, stream=No
     and fp8 weights w [groups, N, K] with scales ws [groups, ceil(N/128),
     ceil(K/128)]; ``offsets`` int32 [groups + 1] on the device (None: one
     group of all rows)."""
-    dev = w.device
+    dev = y.get_device()
     _launch("moe_fp8_linear", dev, stream, ctypes.byref(d),
             _addr(xq, "xq", torch.float8_e4m3fn, d.rows * d.K, dev), _addr(xs, "xs", f32, d.rows * _blocks(d.K), dev),
             _addr(w, "w", torch.float8_e4m3fn, d.groups * d.N * d.K, dev),
@@ -612,7 +628,7 @@ def moe_fp8_linear(d: Linear, xq, xs, w, ws, y, scratch, offsets=None, stream=No
 
 
 def _grouped(fn, d: Linear, a, an, a_name, b, bn, b_name, out, on, out_name, scratch, offsets, stream) -> None:
-    dev = out.device
+    dev = out.get_device()
     t = _TORCH_TYPES[d.in_type]
     _launch(fn, dev, stream, ctypes.byref(d), _addr(a, a_name, t, an, dev), _addr(b, b_name, t, bn, dev),
             _offsets(d, offsets, dev), _addr(out, out_name, _TORCH_TYPES[d.out_type], on, dev),

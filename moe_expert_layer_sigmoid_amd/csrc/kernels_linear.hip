@@ -54,6 +54,11 @@ __device__ __forceinline__ v4f mfma8(v8i a, v8i b, v4f c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kFmtFp8, kFmtFp8, 0, 0, 0, 0);
 }
 
+// A 16-byte store at any multiple of the output type's size (rows of an odd
+// number of 16-bit values start at odd multiples of 2 bytes).
+typedef v4i v4i_any __attribute__((aligned(2)));
+__device__ __forceinline__ void store16(void* p, v4i v) { *static_cast<v4i_any*>(p) = v; }
+
 // Rows [lo, hi) of group g.  Offsets outside [0, rows], or falling, break the
 // caller's contract; they are clamped so that no row outside the tensors is
 // touched.
@@ -107,32 +112,38 @@ __device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int r
 }
 
 // Shape of a block's work.  TA x TB: columns x rows of its output tile; WA x WB
-// waves; NS: stages of the LDS ring; OCC: blocks per compute unit the
+// waves; KS: teams of that many waves, each with its own LDS ring and every
+// KS-th stage; NS: stages of a ring; OCC: blocks per compute unit the
 // registers must allow.
-template <int IN_, int OP_, int TA_, int TB_, int WA_, int WB_, int NS_, int OCC_>
+template <int IN_, int OP_, int TA_, int TB_, int WA_, int WB_, int KS_, int NS_, int OCC_>
 struct Shape {
-  static constexpr int IN = IN_, OP = OP_, TA = TA_, TB = TB_, WA = WA_, WB = WB_, NS = NS_, OCC = OCC_;
+  static constexpr int IN = IN_, OP = OP_, TA = TA_, TB = TB_, WA = WA_, WB = WB_, KS = KS_, NS = NS_, OCC = OCC_;
   static constexpr int W = WA * WB;
   static constexpr int ES = IN == kFP8 ? 1 : 2;
   static constexpr int RE = 128 / ES;               // reduction elements per stage
   static constexpr bool AT = OP != kFwd;            // operand stored with its columns contiguous (read transposed)
   static constexpr bool BT = OP == kDw;
   static constexpr int TI = TA / WA / 16, TJ = TB / WB / 16;  // 16 x 16 tiles per wave
-  static constexpr int PG = TI < 4 ? TI : 4;        // A tiles whose columns interleave (below)
-  static constexpr int PGS = 4 * PG;
   static constexpr int NA = TA / 8 / W, NB = TB / 8 / W;      // 1 KB DMA instructions per wave and stage
-  static constexpr int NI = NA + NB + (IN == kFP8 ? 1 : 0);
-  static constexpr int kScale = IN == kFP8 ? W * 256 : 0;
-  static constexpr int kSlot = (TA + TB) * 128 + kScale;
+  static constexpr int NI = NA + NB;
+  static constexpr int kSlot = (TA + TB) * 128;
+  // fp8 scales: two buffers of four stages' values: 16 bytes a row, then 16
+  // bytes per 128 columns (written by whole waves)
+  static constexpr int kRowSc = (TB < 64 ? 64 : TB) * 16;
+  static constexpr int kScale = IN == kFP8 ? kRowSc + 1024 : 0;
+  static constexpr int kTeam = NS * kSlot + 2 * kScale;  // LDS of a team
   static constexpr int PRE = NS - 1;
   static constexpr int U = IN == kFP8 ? TI : 2 * TI;  // steps of a stage (below)
   static constexpr int D = IN == kFP8 ? 2 : 3;        // steps that operands are read ahead
+  static constexpr int P = NS == 2 ? U / 2 : U;       // steps that the next DMA is issued in
   static constexpr int kLag = TJ == 1 ? 2 : 3;
   static_assert(U % 4 == 0 && D < 4 && kLag < 4 && (IN != kFP8 || kLag <= (U - D) * TJ), "rings of four");
   static_assert(NA * W * 8 == TA && NB * W * 8 == TB && TI * WA * 16 == TA && TJ * WB * 16 == TB, "tile shape");
-  static_assert(PRE * NI < 64, "vmcnt range");
+  static_assert(PRE * NI + 1 < 64, "vmcnt range");
   static_assert(IN != kFP8 || TB / 64 < W, "a wave for the weight scales");
-  static_assert(NS * kSlot <= 160 * 1024, "LDS");
+  static_assert(KS * kTeam <= 160 * 1024, "LDS");
+  static_assert(KS == 1 || TA * TB * 4 <= NS * kSlot, "a team's sums fit its ring");
+  static_assert(KS == 1 || KS == 2, "teams share groups of four stages");
 };
 
 struct Plan {
@@ -144,13 +155,13 @@ struct Plan {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearArgs p, Plan pl) {
+__global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) k_linear(LinearArgs p, Plan pl) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the kernel's name alone, and not every device builtin type-checks there
   constexpr int TA = C::TA, TB = C::TB, TI = C::TI, TJ = C::TJ, W = C::W, ES = C::ES, NS = C::NS, PRE = C::PRE;
   constexpr int IN = C::IN, OP = C::OP;
-  __shared__ __align__(1024) uint8_t ring[NS * C::kSlot];
+  __shared__ __align__(1024) uint8_t ring[C::KS * C::kTeam];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int team = __builtin_amdgcn_readfirstlane(tid >> 6) / W, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W;
   const int l16 = lane & 15, q = lane >> 4;
   const int wa = wave % C::WA, wb = wave / C::WA;
   const int cols = OP == kFwd ? p.N : p.K;
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     }
   }
   const int nst = (nred + C::RE - 1) / C::RE;
-  int s_lo, s_n;  // the block's stages
+  int s_lo, s_n;  // the block's stages; its teams take them in turn
   {
     const int sps = OP == kDw ? (nst + pl.splits - 1) / pl.splits : pl.sps;
     s_lo = min(nst, split * sps);
@@ -229,10 +240,7 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
   // Lane offsets of an operand's first instruction; instruction m is a uniform
   // distance further.  (Rows 32 apart permute their pieces alike.)
   auto kc_row = [&]() { return 8 * wave + (lane >> 3); };
-  auto kc_piece = [&](bool perm) {
-    const int row = kc_row();
-    return (lane & 7) ^ (perm ? (row & 3) | (((row / C::PGS) & 1) << 2) : row & 7);
-  };
+  auto kc_piece = [&]() { return (lane & 7) ^ (kc_row() & 7); };
   auto mc_off = [&](int T, int ld, int ncol) {
     const int PR = T / 8, RPI = 64 / PR;  // pieces per row, rows per instruction
     const int row = wave * RPI + lane / PR;
@@ -240,18 +248,21 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     const int pc = (lane % PR) ^ ((2 * f) & (PR - 1));
     return 8 * pc < ncol ? ((uint32_t)row * (uint32_t)ld + 8u * pc) * 2u : kOob;
   };
-  const uint32_t apc = 16u * (uint32_t)kc_piece(true), bpc = 16u * (uint32_t)kc_piece(false);
+  const uint32_t kpc = 16u * (uint32_t)kc_piece();
   const uint32_t rowb = (uint32_t)(ldr * ES);
-  const uint32_t avo = C::AT ? mc_off(TA, p.K, cols - c0) : (uint32_t)kc_row() * rowb + apc;
-  const uint32_t bvo = C::BT ? mc_off(TB, p.N, nr) : (uint32_t)kc_row() * rowb + bpc;
+  const uint32_t avo = C::AT ? mc_off(TA, p.K, cols - c0) : (uint32_t)kc_row() * rowb + kpc;
+  const uint32_t bvo = C::BT ? mc_off(TB, p.N, nr) : (uint32_t)kc_row() * rowb + kpc;
   const uint32_t astep = C::AT ? (uint32_t)(W * (512 / TA) * p.K * 2) : 8 * W * rowb;
   const uint32_t bstep = C::BT ? (uint32_t)(W * (512 / TB) * p.N * 2) : 8 * W * rowb;
 
-  // fp8 scales: one dword per lane and stage; waves [0, TB / 64): the rows',
-  // the last wave: the weights', per 128 columns of the tile
+  // fp8 scales, four stages at a time, 16 bytes a lane: waves [0, TB / 64) load
+  // the rows', the last wave the weights' of each 128 columns of the tile.
+  // (A dword a row and stage, 64 lines an instruction, kept the address unit
+  // busy: 8192 x 4096 x 7168 took 8 % longer.)
   const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
   const float* scp = nullptr;
   uint32_t sclim = 0, scvo = kOob;
+  const bool scw = IN == kFP8 && (wave < (TB + 63) / 64 || wave == W - 1);
   if constexpr (IN == kFP8) {
     if (wave < (TB + 63) / 64) {
       scp = p.bs + (size_t)r0 * nkb;
@@ -268,14 +279,20 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
                                                      (uint32_t)__builtin_amdgcn_readfirstlane((int)a)));
     sclim = (uint32_t)__builtin_amdgcn_readfirstlane((int)sclim);
   }
+  auto dma_scales = [&](lds_u8* dst, int st) __attribute__((always_inline)) {  // of stages st .. st + 3
+    // the stage goes into the checked offset: a row's last four may end past it
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(scp, sclim),
+                                             (lds_void)(dst + (wave == W - 1 ? C::kRowSc : wave * 1024)), 16,
+                                             scvo + (uint32_t)st * 4u, 0, 0, 0);
+  };
 
   // DMA instruction m of stage st into a ring slot.  Stages past the end load
   // nothing (their buffers have no bytes), so that every stage counts the
   // same number of loads.
   auto dma = [&](lds_u8* wr, int st, int m, bool live) __attribute__((always_inline)) {
-    auto kc = [&](const uint8_t* base, uint32_t lim, uint32_t vo, uint32_t pc, uint32_t step, int m, lds_u8* dst) {
+    auto kc = [&](const uint8_t* base, uint32_t lim, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
       const uint32_t so = (uint32_t)st * 128u;
-      const uint32_t v = so + pc < rowb ? vo : kOob;  // pieces past the row's end
+      const uint32_t v = so + kpc < rowb ? vo : kOob;  // pieces past the row's end
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, live ? lim : 0u), (lds_void)(dst + (wave + W * m) * 1024), 16,
                                                v + (uint32_t)m * step, so, 0, 0);
     };
@@ -287,25 +304,19 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     };
     if (m < C::NA) {
       if (C::AT) mc(abase, p.K, c0, avo, astep, m, wr);
-      else kc(abase, alim, avo, apc, astep, m, wr);
+      else kc(abase, alim, avo, astep, m, wr);
     } else if (m < C::NA + C::NB) {
       if (C::BT) mc(bbase, p.N, r0, bvo, bstep, m - C::NA, wr + TA * 128);
-      else kc(bbase, blim, bvo, bpc, bstep, m - C::NA, wr + TA * 128);
-    } else if constexpr (IN == kFP8) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(scp, live ? sclim : 0u),
-                                               (lds_void)(wr + (TA + TB) * 128 + wave * 256), 4, scvo, (uint32_t)st * 4u,
-                                               0, 0);
+      else kc(bbase, blim, bvo, bstep, m - C::NA, wr + TA * 128);
     }
   };
 
   // ---- LDS reads.  Contiguous reduction: lane (l16, q) of a tile reads pieces
-  // q and q + 4 of its row.  A's tiles interleave their columns (tile i, row
-  // 4 u + e is column PGS u + 4 i + e), so that a lane ends with PGS
-  // consecutive columns.  Transposed: a 16-lane group reads four reduction
+  // q and q + 4 of its row.  Transposed: a 16-lane group reads four reduction
   // rows of 16 columns, each lane getting one column's four values.
-  const int fa = C::AT ? (l16 >> 2) | ((q & 1) << 2) : (l16 & 3) | (((l16 >> 2) & 1) << 2);
+  const int fa = C::AT ? (l16 >> 2) | ((q & 1) << 2) : l16 & 7;
   const int fb = C::BT ? (l16 >> 2) | ((q & 1) << 2) : l16 & 7;
-  const uint32_t ra = (uint32_t)(wa * TI * 16 + C::PGS * (l16 >> 2) + (l16 & 3)) * 128;
+  const uint32_t ra = (uint32_t)(wa * TI * 16 + l16) * 128;
   const uint32_t rb = (uint32_t)(TA * 128 + (wb * TJ * 16 + l16) * 128);
   auto ld_kc = [&](const lds_u8* rd, uint32_t row, int kk, int f) {
     return *reinterpret_cast<const lds_v4i*>(rd + row + (((4 * kk + q) ^ f) * 16));
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
   };
   auto lda = [&](const lds_u8* rd, int i, int kk) {
     if constexpr (C::AT) return ld_mc(rd, TA, wa * TI + i, kk, fa);
-    else return ld_kc(rd, ra + (uint32_t)((i / C::PG) * C::PG * 16 + (i % C::PG) * 4) * 128, kk, fa);
+    else return ld_kc(rd, ra + (uint32_t)(i * 16) * 128, kk, fa);
   };
   auto ldb = [&](const lds_u8* rd, int j, int kk) {
     if constexpr (C::BT) return ld_mc(rd + TA * 128, TB, wb * TJ + j, kk, fb);
@@ -338,7 +349,10 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
   // read D steps ahead, and the last D steps of a stage run after the barrier
   // that ends it, from registers, while the next stage's first operands are on
   // their way: no wave stands at the start of a stage waiting for LDS.  The
-  // next DMA is issued in between, instruction by instruction.  fp8: a tile's
+  // next DMA is issued in between, instruction by instruction: over the whole
+  // stage in a deeper ring, over its first half in one of two stages, where it
+  // has to land by the stage's end (bf16 8192^3: 869 us over all of it, 799
+  // over half, 802 over a quarter).  fp8: a tile's
   // product is scaled and added kLag products later, when it is long finished.
   constexpr int U = C::U, D = C::D, kLag = C::kLag;
   constexpr int KH = U / TI;  // halves of a stage
@@ -398,9 +412,14 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
   };
 
   // From one barrier to the next: stage s's slot rd is complete, wr is free.
-  auto body = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, int s) __attribute__((always_inline)) {
-    const int st = s_lo + s + PRE;
-    const bool live = s + PRE < s_n;
+  // (swr, srd: the scales' buffers of the next and this group of four stages.)
+  constexpr int kGroup = 4 / C::KS;  // this team's stages of a group
+  auto body = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, lds_u8* __restrict__ swr,
+                  const lds_u8* __restrict__ srd, int s) __attribute__((always_inline)) {
+    const int k = (s + PRE) * C::KS + team, st = s_lo + k;
+    const bool live = k < s_n;
+    if constexpr (IN == kFP8)  // before the stage's tiles, with which they are waited for
+      if (scw && (s < 0 ? s == -PRE : s % kGroup == 0)) dma_scales(swr, s_lo + (s < 0 ? 0 : (s / kGroup + 1) * 4));
     if (s < 0) {
 #pragma unroll
       for (int m = 0; m < C::NI; ++m) dma(wr, st, m, live);
@@ -410,15 +429,15 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     for (int v = 0; v < U; ++v) {
 #pragma unroll
       for (int m = 0; m < C::NI; ++m)
-        if (m * U / C::NI == v) dma(wr, st, m, live);
+        if (m * C::P / C::NI == v) dma(wr, st, m, live);
       if constexpr (IN == kFP8) {
-        const lds_f32* sc = reinterpret_cast<const lds_f32*>(rd + (TA + TB) * 128);
         if (v == 0) {
-          wsc = sc[(W - 1) * 64 + (wa * TI * 16) / 128];
+          const lds_f32* sc = reinterpret_cast<const lds_f32*>(srd) + ((s * C::KS + team) & 3);
+          wsc = sc[C::kRowSc / 4 + 4 * ((wa * TI * 16) / 128)];
 #pragma unroll
           for (int j = 0; j < TJ; ++j) {
             sold[j] = snew[j];
-            snew[j] = sc[wb * TJ * 16 + 16 * j + l16];
+            snew[j] = sc[4 * (wb * TJ * 16 + 16 * j + l16)];
           }
         }
         if (v == D) {
@@ -429,9 +448,11 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
       step((v + U - D) % U, rd, true);
     }
   };
-  lds_u8* const ring0 = (lds_u8*)ring;
+  lds_u8* const ring0 = (lds_u8*)ring + team * C::kTeam;
+  lds_u8* const scale0 = ring0 + NS * C::kSlot;
+  const int steps = (s_n + C::KS - 1) / C::KS;
   int wslot = 0, rslot = 0;
-  for (int s = -PRE; s < s_n; ++s) {
+  for (int s = -PRE; s < steps; ++s) {
     if (s >= 0) {
       // this wave's part of stage s has landed (PRE - 1 younger stages may be
       // in flight) and its reads of stage s - 1 are done; then the barrier
@@ -440,7 +461,8 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
-    body(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, s);
+    const int par = s < 0 ? 1 : (s / kGroup) & 1;  // the prologue's group goes into buffer 0
+    body(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, scale0 + (par ^ 1) * C::kScale, scale0 + par * C::kScale, s);
     wslot = wslot == NS - 1 ? 0 : wslot + 1;
     if (s >= 0) rslot = rslot == NS - 1 ? 0 : rslot + 1;
   }
@@ -454,44 +476,200 @@ __global__ void __launch_bounds__(C::W * 64, C::OCC * C::W / 4) k_linear(LinearA
     for (int n = U * TJ - kLag; n < U * TJ; ++n) promote(n);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
+  if constexpr (C::KS > 1) {
+    // the teams' sums, added in order by the first
+    __syncthreads();
+    lds_f32* const sums = reinterpret_cast<lds_f32*>((lds_u8*)ring);
+    typedef __attribute__((address_space(3))) v4f lds_v4f;
+    auto at = [&](int t, int i, int j) {
+      return reinterpret_cast<lds_v4f*>(sums + t * (C::kTeam / 4) + (((wave * TI + i) * TJ + j) * 64 + lane) * 4);
+    };
+    if (team > 0) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) *at(team, i, j) = acc[i][j];
+    }
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int t = 1; t < C::KS; ++t)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] += *at(t, i, j);
+  }
 
-  // ---- the tile's values, rounded once to the output type
+  // ---- the tile's values, rounded once to the output type.  Each wave turns
+  // its 16-row strips in LDS (its share of the ring, two strips in turn), so
+  // that a store writes whole rows of the wave's columns.  (A lane's own 4 to
+  // 16 consecutive columns stored directly: SEEBELOW.)
+  __syncthreads();
+  constexpr int CW = TI * 16;               // the wave's columns
+  constexpr int kStrip = 16 * CW * 4;
+  static_assert(2 * kStrip * W <= NS * C::kSlot, "strips fit the ring");
+  typedef __attribute__((address_space(3))) v4f lds_v4f;
+  lds_u8* const strip0 = (lds_u8*)ring + wave * 2 * kStrip;
   auto write = [&](auto outc, void* out) {
     constexpr int OUT = decltype(outc)::value;
     using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
-    constexpr int V = C::AT ? 4 : C::PGS;  // consecutive columns of a lane
+    constexpr int V = 16 / sizeof(O);       // columns of a 16-byte store
+    constexpr int LR = CW / V, RI = 64 / LR;  // lanes a row, rows an instruction
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int r = wb * TJ * 16 + 16 * j + l16;
-      if (r >= nr) continue;
+      lds_u8* const strip = strip0 + (j & 1) * kStrip;
+      // 16-byte chunk c of row r lies at chunk c ^ r: no two rows on one bank
 #pragma unroll
-      for (int u = 0; u < TI * 4 / V; ++u) {
-        const int c = wa * TI * 16 + (C::AT ? 16 * u + 4 * q : C::PG * 16 * u + V * q);
-        O v[V];
+      for (int i = 0; i < TI; ++i)
+        *reinterpret_cast<lds_v4f*>(strip + l16 * CW * 4 + ((4 * i + q) ^ l16) * 16) = acc[i][j];
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i)
+      for (int k = 0; k < 16 / RI; ++k) {
+        const int rr = k * RI + lane / LR, c = (lane % LR) * V;
+        const int r = wb * TJ * 16 + 16 * j + rr, cc = wa * CW + c;
+        O* o = static_cast<O*>(out) + out0 + (size_t)r * cols + cc;
+        if (r < nr) {
+          if (c0 + cc + V <= cols) {
+            O v[V];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * i + e] = (O)acc[u * (V / 4) + i][j][e];
-        O* o = static_cast<O*>(out) + out0 + (size_t)r * cols + c;
-        if (c0 + c + V <= cols) {
-          __builtin_memcpy(o, v, sizeof v);  // rows start at any multiple of the type's size
-        } else {
+            for (int h = 0; h < V / 4; ++h) {
+              const v4f x = *reinterpret_cast<const lds_v4f*>(strip + rr * CW * 4 + ((c / 4 + h) ^ rr) * 16);
 #pragma unroll
-          for (int e = 0; e < V; ++e)
-            if (c0 + c + e < cols) o[e] = v[e];
+              for (int e = 0; e < 4; ++e) v[4 * h + e] = (O)x[e];
+            }
+            v4i w;
+            __builtin_memcpy(&w, v, 16);
+            store16(o, w);
+          } else {
+#pragma unroll 1
+            for (int e = 0; c0 + cc + e < cols; ++e)
+              o[e] = (O) * reinterpret_cast<const lds_f32*>(strip + rr * CW * 4 + (((c + e) / 4) ^ rr) * 16 + (e & 3) * 4);
+          }
         }
       }
     }
   };
-  if (pl.splits > 1) {
+  if (pl.splits > 1 || pl.out_type == kF32) {
     const size_t total = (size_t)(OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;
-    write(std::integral_constant<int, kF32>{}, static_cast<float*>(p.part) + split * total);
-  } else if (pl.out_type == kF32) {
-    write(std::integral_constant<int, kF32>{}, p.out);
+    write(std::integral_constant<int, kF32>{}, pl.splits > 1 ? static_cast<float*>(p.part) + split * total : p.out);
   } else if (IN == kF16 || (IN == kFP8 && pl.out_type == kF16)) {
     write(std::integral_constant<int, kF16>{}, p.out);
   } else {
     write(std::integral_constant<int, kBF16>{}, p.out);
+  }
+#endif
+}
+
+// ---- few rows: y for at most 16 TJ rows of a group at a time.  The weights
+// are read once, straight into the MFMA's operand registers: a block takes
+// 16 TI columns, its eight waves every eighth 128-byte piece of the rows, each
+// a chunk of CH pieces ahead; the waves' sums are added in order through LDS.
+// One launch, no partial sums in memory, and columns / 16 TI blocks a group.
+constexpr int kFewWaves = 8;
+
+template <int IN, int TI, int TJ, int CH>
+__global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int out_type) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int ES = IN == kFP8 ? 1 : 2;
+  __shared__ __align__(16) float red[kFewWaves][TI * TJ][256];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int g = blockIdx.y, c0 = blockIdx.x * 16 * TI;
+  int lo, hi;
+  group_rows(p.off, g, p.rows, lo, hi);
+  const uint32_t rowb = (uint32_t)(p.K * ES);
+  const int npc = (int)(rowb + 127) / 128;  // 128-byte pieces of a row
+  const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
+  const rsrc_t Ar = make_rsrc(static_cast<const uint8_t*>(p.a) + ((size_t)g * p.N + c0) * rowb,
+                              (uint32_t)min(16 * TI, p.N - c0) * rowb);
+  const float* wsp = IN == kFP8 ? p.as + ((size_t)g * nnb + c0 / 128) * nkb : nullptr;
+  for (int r0 = lo; r0 < hi; r0 += 16 * TJ) {
+    const int nr = min(16 * TJ, hi - r0);
+    const rsrc_t Br = make_rsrc(static_cast<const uint8_t*>(p.b) + (size_t)r0 * rowb, (uint32_t)nr * rowb);
+    const rsrc_t Sr = make_rsrc(IN == kFP8 ? p.bs + (size_t)r0 * nkb : nullptr, IN == kFP8 ? (uint32_t)(nr * nkb) * 4u : 0u);
+    const rsrc_t Tr = make_rsrc(wsp, IN == kFP8 ? (uint32_t)nkb * 4u : 0u);
+    v4f acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    struct Piece {
+      v4i a[TI][2], b[TJ][2];
+      int xs[TJ], ws;
+    };
+    Piece buf[2][CH];
+    // piece pc of the row: lane (l16, q) takes bytes [16 q, 16 q + 16) and the
+    // same of its upper half; past the row's or the tensor's end, zeros
+    auto fetch = [&](Piece& x, int pc) {
+      const uint32_t o = (uint32_t)pc * 128u + 16u * q;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = o + 64u * h < rowb;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+          x.a[i][h] = buf_load16_p<2>(Ar, in ? (uint32_t)(16 * i + l16) * rowb + o + 64u * h : kOob, 0);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          x.b[j][h] = buf_load16(Br, in ? (uint32_t)(16 * j + l16) * rowb + o + 64u * h : kOob, 0);
+      }
+      if constexpr (IN == kFP8) {
+        x.ws = buf_load4(Tr, pc < nkb ? 4u * pc : kOob, 0);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          x.xs[j] = buf_load4(Sr, pc < nkb ? (uint32_t)((16 * j + l16) * nkb + pc) * 4u : kOob, 0);
+      }
+    };
+    auto add = [&](const Piece& x) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        if constexpr (IN == kFP8) {
+          const float s = __int_as_float(x.xs[j]) * __int_as_float(x.ws);
+#pragma unroll
+          for (int i = 0; i < TI; ++i) {
+            const v8i a = __builtin_shufflevector(x.a[i][0], x.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const v8i b = __builtin_shufflevector(x.b[j][0], x.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const v4f d = mfma8(a, b, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TI; ++i) acc[i][j] = mfma16<IN>(x.a[i][h], x.b[j][h], acc[i][j]);
+        }
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < CH; ++k) fetch(buf[0][k], wave + kFewWaves * k);
+    for (int p0 = wave; p0 < npc; p0 += 2 * CH * kFewWaves) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int base = p0 + h * CH * kFewWaves;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) fetch(buf[h ^ 1][k], base + (CH + k) * kFewWaves);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) add(buf[h][k]);
+      }
+    }
+    if (r0 > lo) __syncthreads();  // the sums of the rows before have been read
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(&red[wave][i * TJ + j][l16 * 16 + 4 * q]) = acc[i][j];
+    __syncthreads();
+    for (int t = tid; t < TI * TJ * 256; t += kFewWaves * 64) {
+      const int tile = t >> 8, r = (tile % TJ) * 16 + ((t >> 4) & 15), c = c0 + (tile / TJ) * 16 + (t & 15);
+      float s = red[0][tile][t & 255];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) s += red[w][tile][t & 255];
+      if (r < nr && c < p.N) {
+        const size_t o = (size_t)(r0 + r) * p.N + c;
+        if (out_type == kF32) static_cast<float*>(p.out)[o] = s;
+        else if (out_type == kF16) static_cast<_Float16*>(p.out)[o] = (_Float16)s;
+        else static_cast<__bf16*>(p.out)[o] = (__bf16)s;
+      }
+    }
   }
 #endif
 }
@@ -530,10 +708,15 @@ constexpr int kMaxSplits = 16;
 constexpr int kCus = 256;
 
 // Tile shapes, largest first (columns x rows of the output): index, TA, TB
-constexpr int kShapes = 4;
-constexpr int kTA[kShapes] = {256, 256, 128, 128}, kTB[kShapes] = {256, 128, 64, 32};
+constexpr int kShapes = 8;
+constexpr int kTA[kShapes] = {256, 256, 128, 128, 128, 128, 128, 128}, kTB[kShapes] = {256, 128, 64, 32, 64, 32, 128, 128};
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Rows a group on average up to which the forward product takes k_linear_few.
+bool few_rows(int rows, int groups) {
+  return rows <= 16;
+}
 
 struct Choice {
   int shape;
@@ -568,6 +751,7 @@ Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
 }
 
 size_t part_bytes(int op, int in_type, int rows, int N, int K, int groups) {
+  if (op == kFwd && few_rows(rows, groups)) return 0;
   const Choice c = choose(op, in_type, rows, N, K, groups);
   if (c.plan.splits == 1) return 0;
   const size_t out = op == kFwd ? (size_t)rows * N : (op == kDx ? (size_t)rows * K : (size_t)groups * N * K);
@@ -579,7 +763,7 @@ hipError_t run_shape(const LinearArgs& p, const Plan& pl, hipStream_t st) {
   long blocks;
   if (C::OP == kDw) blocks = (long)p.groups * (ceil_div(pl.nca * pl.nrb * pl.splits, kXcd) * kXcd);
   else blocks = (long)ceil_div(pl.nca * pl.nrb * pl.splits, kXcd) * kXcd;
-  k_linear<C><<<dim3((unsigned)blocks), C::W * 64, 0, st>>>(p, pl);
+  k_linear<C><<<dim3((unsigned)blocks), C::KS * C::W * 64, 0, st>>>(p, pl);
   return hipGetLastError();
 }
 
@@ -589,10 +773,20 @@ hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   c.plan.out_type = out_type;
   p.part = ws;
   hipError_t e;
-  if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 2, 1>>(p, c.plan, st);
-  else if (c.shape == 1) e = run_shape<Shape<IN, OP, 256, 128, 4, 2, 3, 1>>(p, c.plan, st);
-  else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 3, 2>>(p, c.plan, st);
-  else e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 3, 2>>(p, c.plan, st);
+  if (OP == kFwd && few_rows(p.rows, p.groups)) {
+    const int avg = ceil_div(p.rows, p.groups);
+    if (avg <= 16) k_linear_few<IN, 1, 1, 4><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
+    else k_linear_few<IN, 1, 2, 2><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
+    return hipGetLastError();
+  }
+  if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 1, 2, 1>>(p, c.plan, st);
+  else if (c.shape == 1) e = run_shape<Shape<IN, OP, 256, 128, 4, 2, 1, 3, 1>>(p, c.plan, st);
+  else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 1, 3, 2>>(p, c.plan, st);
+  else if (c.shape == 4) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 2, 3, 1>>(p, c.plan, st);
+  else if (c.shape == 5) e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 2, 3, 1>>(p, c.plan, st);
+  else if (c.shape == 6) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 1, 2, 2>>(p, c.plan, st);
+  else if (c.shape == 7) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 2, 2, 1>>(p, c.plan, st);
+  else e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 1, 3, 2>>(p, c.plan, st);
   if (e != hipSuccess || c.plan.splits == 1) return e;
   const int cols = OP == kFwd ? p.N : p.K;
   const size_t total = (OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;

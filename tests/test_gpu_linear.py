@@ -122,6 +122,22 @@ def test_swiglu_quant(rows, K, dt):
     assert np.all(err <= np.abs(h) * (2.0 ** -4 + 2 * rel) + sv * 2.0 ** -10 + 1e-30)
 
 
+def test_swiglu_of_infinities():
+    """silu(inf) = inf, silu(-inf) = -inf * 0 = NaN, and inf * 0 = NaN: a block
+    holding one has an infinite or NaN scale; the other blocks keep theirs."""
+    x = torch.ones(4, 512, device="cuda")
+    x[0, 3], x[1, 3], x[2, 3], x[2, 259] = float("inf"), -float("inf"), float("inf"), 0.0
+    x[3, :256] = 120.0
+    q = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(4, 2, device="cuda")
+    mx.moe_fp8_swiglu_quant(x, q, s)
+    s = s.cpu()
+    one = np.float32(1 / (1 + np.exp(-1.0)))
+    assert torch.isinf(s[0, 0]) and torch.isnan(s[1, 0]) and torch.isnan(s[2, 0])
+    assert torch.all((s[:3, 1] * 448 - one).abs() < 1e-6)
+    assert torch.all(s[3] == 120.0 / 448) and torch.all(q[3].float() == 448)
+
+
 def test_quant_rows_further_apart_and_other_stream():
     base = _t(_rng(3).standard_normal((7, 512)), torch.bfloat16)
     x = base[:, 64:64 + 144]
@@ -178,7 +194,8 @@ FP8 = [  # rows, groups, N, K, empty groups
     (1, 1, 33, 64, ()), (1, 1, 512, 2048, ()), (2, 1, 129, 16, ()), (7, 1, 255, 400, ()), (16, 1, 96, 1152, ()),
     (17, 1, 130, 144, ()), (33, 1, 257, 272, ()), (64, 1, 64, 256, ()), (77, 1, 261, 528, ()), (130, 1, 200, 128, ()),
     (300, 1, 300, 384, ()), (1, 4, 48, 160, ()), (5, 9, 130, 256, (0, 8)), (40, 3, 257, 144, (1,)),
-    (150, 5, 140, 272, (2, 3)), (400, 2, 260, 256, ()), (3, 70, 40, 128, ())]
+    (150, 5, 140, 272, (2, 3)), (400, 2, 260, 256, ()), (3, 70, 40, 128, ()),
+    (100, 8, 50, 1200, (3,)), (16, 1, 17, 32768, ())]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
@@ -273,7 +290,8 @@ def test_fp8_linear_keeps_other_groups_and_rows_apart():
 GROUPED = [  # rows, groups, N, K, empty groups
     (1, 1, 64, 64, ()), (1, 1, 8, 8, ()), (1, 3, 72, 2056, (0, 2)), (9, 1, 264, 392, ()), (16, 1, 72, 1096, ()),
     (31, 2, 136, 200, ()), (66, 1, 520, 72, ()), (128, 8, 256, 256, ()), (250, 9, 264, 392, (4,)),
-    (300, 1, 200, 328, ()), (520, 2, 72, 136, (0,)), (515, 3, 264, 264, ()), (3, 70, 24, 40, ())]
+    (300, 1, 200, 328, ()), (520, 2, 72, 136, (0,)), (515, 3, 264, 264, ()), (3, 70, 24, 40, ()),
+    (100, 8, 56, 1192, (3,))]
 
 
 def _case16(rng, dt, rows, groups, N, K, empty):
