@@ -15,6 +15,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <math.h>
 
 #include <type_traits>
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   // bands of four column tiles, row by row, so that the 32 tiles a die works
   // on at one time read about 4 column and 8 row operands.
   int g, lo, hi, c0, r0, nr, nred, split;
-  size_t out0;
+  size_t row0;  // the tile's first row in the output
   {
     const int xcd = blockIdx.x % kXcd, j = blockIdx.x / kXcd;
     if (OP == kDw) {
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       c0 = (4 * band + rem % w) * TA;
       nr = min(TB, p.N - r0);
       nred = hi - lo;
-      out0 = ((size_t)g * p.N + r0) * p.K + c0;
+      row0 = (size_t)g * p.N + r0;
     } else {
       const int tiles = count_tiles<TB>(p.off, p.groups, p.rows) * pl.nca;
       const int items = tiles * pl.splits, share = (items + kXcd - 1) / kXcd;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       c0 = (4 * band + rem % w) * TA;
       nr = min(TB, hi - r0);
       nred = OP == kFwd ? p.K : p.N;
-      out0 = (size_t)r0 * cols + c0;
+      row0 = (size_t)r0;
     }
   }
   const int nst = (nred + C::RE - 1) / C::RE;
@@ -503,14 +504,15 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   // ---- the tile's values, rounded once to the output type.  Each wave turns
   // its 16-row strips in LDS (its share of the ring, two strips in turn), so
   // that a store writes whole rows of the wave's columns.  (A lane's own 4 to
-  // 16 consecutive columns stored directly: SEEBELOW.)
+  // 16 consecutive columns stored directly: 8192 x 4096 x 7168 in fp8 215 us
+  // against 205, the weight gradients of 4 experts of 7168 x 2048 157 against 128.)
   __syncthreads();
   constexpr int CW = TI * 16;               // the wave's columns
   constexpr int kStrip = 16 * CW * 4;
   static_assert(2 * kStrip * W <= NS * C::kSlot, "strips fit the ring");
   typedef __attribute__((address_space(3))) v4f lds_v4f;
   lds_u8* const strip0 = (lds_u8*)ring + wave * 2 * kStrip;
-  auto write = [&](auto outc, void* out) {
+  auto write = [&](auto outc, void* out, int pitch) {
     constexpr int OUT = decltype(outc)::value;
     using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
     constexpr int V = 16 / sizeof(O);       // columns of a 16-byte store
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       for (int k = 0; k < 16 / RI; ++k) {
         const int rr = k * RI + lane / LR, c = (lane % LR) * V;
         const int r = wb * TJ * 16 + 16 * j + rr, cc = wa * CW + c;
-        O* o = static_cast<O*>(out) + out0 + (size_t)r * cols + cc;
+        O* o = static_cast<O*>(out) + (row0 + r) * pitch + c0 + cc;
         if (r < nr) {
           if (c0 + cc + V <= cols) {
             O v[V];
@@ -549,12 +551,14 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
     }
   };
   if (pl.splits > 1 || pl.out_type == kF32) {
-    const size_t total = (size_t)(OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;
-    write(std::integral_constant<int, kF32>{}, pl.splits > 1 ? static_cast<float*>(p.part) + split * total : p.out);
+    // partial sums: rows padded to 16 bytes
+    const int pitch = pl.splits > 1 ? (cols + 3) & ~3 : cols;
+    const size_t total = (size_t)(OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * pitch;
+    write(std::integral_constant<int, kF32>{}, pl.splits > 1 ? static_cast<float*>(p.part) + split * total : p.out, pitch);
   } else if (IN == kF16 || (IN == kFP8 && pl.out_type == kF16)) {
-    write(std::integral_constant<int, kF16>{}, p.out);
+    write(std::integral_constant<int, kF16>{}, p.out, cols);
   } else {
-    write(std::integral_constant<int, kBF16>{}, p.out);
+    write(std::integral_constant<int, kBF16>{}, p.out, cols);
   }
 #endif
 }
@@ -674,88 +678,138 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
 #endif
 }
 
-// out = sum of the splits' partial sums, in split order.  kFwd, kDx: rows in
-// no group have none and are left alone.
+// out = sum of the splits' partial sums, in split order, four columns a thread;
+// four splits' loads are in flight at a time.  kFwd, kDx: rows in no group have
+// no sums and are left alone.
 template <int OUT>
-__global__ void __launch_bounds__(256) k_linear_join(LinearArgs p, size_t total, int cols, int splits, bool rows_out) {
+__global__ void __launch_bounds__(256) k_linear_join(LinearArgs p, int rows, int cols, int splits, bool rows_out) {
   using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
+  const uint32_t quads = (uint32_t)(cols + 3) / 4;
+  const size_t total = (size_t)rows * quads;
   size_t i0 = 0, i1 = total;
   if (rows_out && p.off) {
-    i0 = (size_t)min(max(p.off[0], 0), p.rows) * cols;
-    i1 = (size_t)min(max(p.off[p.groups], 0), p.rows) * cols;
+    i0 = (size_t)min(max(p.off[0], 0), rows) * quads;
+    i1 = (size_t)min(max(p.off[p.groups], 0), rows) * quads;
   }
-  const bool quad = cols % 4 == 0;  // 4 values a thread: every row and partial starts 16-byte aligned
-  const size_t step = (size_t)gridDim.x * 256, t = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const float* part = static_cast<const float*>(p.part);
-  O* out = static_cast<O*>(p.out);
-  if (quad) {
-    for (size_t i = i0 + 4 * t; i < i1; i += 4 * step) {
-      v4f s = *reinterpret_cast<const v4f*>(part + i);
-      for (int z = 1; z < splits; ++z) s += *reinterpret_cast<const v4f*>(part + z * total + i);
-      O v[4] = {(O)s[0], (O)s[1], (O)s[2], (O)s[3]};
-      __builtin_memcpy(out + i, v, sizeof v);
+  const v4f* part = static_cast<const v4f*>(p.part);
+  for (size_t i = i0 + (size_t)blockIdx.x * 256 + threadIdx.x; i < i1; i += (size_t)gridDim.x * 256) {
+    v4f s = part[i];
+    for (int z = 1; z < splits; z += 4) {
+      v4f x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = part[(size_t)min(z + k, splits - 1) * total + i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (z + k < splits) s += x[k];
     }
-  } else {
-    for (size_t i = i0 + t; i < i1; i += step) {
-      float s = part[i];
-      for (int z = 1; z < splits; ++z) s += part[z * total + i];
-      out[i] = (O)s;
-    }
+    const size_t row = i / quads;
+    const int c = (int)(i - row * quads) * 4;
+    O* o = static_cast<O*>(p.out) + row * cols + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < cols) o[e] = (O)s[e];
   }
 }
 
 constexpr int kMaxSplits = 16;
+constexpr size_t kPartMax = (size_t)64 << 20;  // partial sums of a split reduction, at most
 constexpr int kCus = 256;
 
-// Tile shapes, largest first (columns x rows of the output): index, TA, TB
-constexpr int kShapes = 8;
-constexpr int kTA[kShapes] = {256, 256, 128, 128, 128, 128, 128, 128}, kTB[kShapes] = {256, 128, 64, 32, 64, 32, 128, 128};
+// Block shapes, and what each measured (us; fp8 at 8192 x 4096 x 7168 and 512 x
+// 4096 x 7168, 16-bit within a fifth of it): a stage of a block that has its
+// compute unit to itself on a half-empty card (`alone`), a stage per compute
+// unit with every one full (`full`), and a block's start and end (`edge`).
+struct Cost {
+  int ta, tb, occ;
+  float alone, full, edge;
+};
+constexpr int kShapes = 6;
+constexpr Cost kCost[kShapes] = {
+    {256, 256, 1, 1.15f, 1.73f, 8.0f},    // most arithmetic per byte moved: large products
+    {256, 128, 1, 0.72f, 1.00f, 5.0f},    // groups of about 100 rows: the weights pass through LDS once
+    {128, 128, 2, 0.70f, 0.545f, 4.0f},   // two blocks a compute unit: one stores while the other computes
+    {128, 64, 2, 0.46f, 0.32f, 2.6f},     // fewer rows a group
+    {128, 64, 1, 0.375f, 0.37f, 2.9f},    // the same by two teams: few tiles, a long reduction
+    {128, 32, 2, 0.38f, 0.265f, 2.0f},    // decode: the stream of the weights
+};
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Rows a group on average up to which the forward product takes k_linear_few.
-bool few_rows(int rows, int groups) {
-  return rows <= 16;
-}
 
 struct Choice {
   int shape;
   Plan plan;
 };
 
+// The shape and the number of splits with the smallest estimate of
+//   max(rounds of blocks in sequence, the work at the full card's rate, the
+//   staged bytes at 16 TB/s) + the join of the splits.
+// The groups' sizes are on the device; the estimate takes them as equal, with
+// half a tile of waste each.  (Against timing every shape on the 105 products of
+// three sets of sizes the choice is 4.5 % from the best on average.)
 Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
-  const int es = in_type == kFP8 ? 1 : 2, re = 128 / es;
+  const int re = in_type == kFP8 ? 128 : 64;
   const int cols = op == kFwd ? N : K;
-  const int avg = op == kDw ? N : ceil_div(rows, groups);
-  Choice c{};
-  auto tiles = [&](int s) {
-    const long nca = ceil_div(cols, kTA[s]);
-    const long nrb = op == kDw ? (long)ceil_div(N, kTB[s]) * groups : rows / kTB[s] + (rows < groups ? rows : groups);
-    return nca * (nrb > 0 ? nrb : 1);
-  };
-  int s = avg > 128 ? 0 : (avg > 64 ? 1 : (avg > 32 ? 2 : 3));
-  while (s < 2 && tiles(s) < kCus) ++s;
-  c.shape = s;
-  c.plan.nca = ceil_div(cols, kTA[s]);
-  c.plan.nrb = op == kDw ? ceil_div(N, kTB[s]) : (int)(tiles(s) / c.plan.nca);
-  // split the reduction while the tiles leave compute units idle, at least
-  // four stages a piece
+  const int live = op == kDw ? groups : (rows < groups ? rows : groups);  // groups with rows, at most
   const int nst = ceil_div(op == kFwd ? K : (op == kDx ? N : ceil_div(rows, groups)), re);
-  int split = (int)(kCus / tiles(s));
-  split = split < nst / 4 ? split : nst / 4;
-  split = split < kMaxSplits ? split : kMaxSplits;
-  if (split < 1) split = 1;
-  c.plan.sps = ceil_div(nst > 0 ? nst : 1, split);
-  c.plan.splits = op == kDw ? split : ceil_div(nst > 0 ? nst : 1, c.plan.sps);
-  return c;
+  const float rate = in_type == kFP8 ? 1.0f : 0.85f;
+  const float out = (op == kDw ? (float)groups * N : (float)rows) * ((cols + 3) & ~3);
+  Choice best{};
+  float best_us = 0.0f;
+  for (int s = 0; s < kShapes; ++s) {
+    const Cost& c = kCost[s];
+    const int nca = ceil_div(cols, c.ta);
+    int nrb;      // row tiles a group (kDw) or at most in all
+    float tiles;  // expected in all
+    if (op == kDw) {
+      nrb = ceil_div(N, c.tb);
+      tiles = (float)nrb * nca * groups;
+    } else {
+      nrb = rows / c.tb + live;
+      const float part = live ? (float)rows / live / c.tb : 0.0f;
+      const float each = groups == 1 ? ceilf(part) : 0.5f * (part + 0.5f + ceilf(part));
+      tiles = (each > 1.0f ? each : 1.0f) * live * nca;
+    }
+    static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kMaxSplits};
+    for (const int want : kSplits) {
+      if (want > 1 && (tiles * want > 4 * kCus || want * 4 > nst || out * 4 * want > (float)kPartMax)) break;
+      const int sps = ceil_div(nst > 0 ? nst : 1, want);
+      const int splits = op == kDw ? want : ceil_div(nst > 0 ? nst : 1, sps);
+      const float blocks = tiles * splits, rounds = ceilf(blocks / (kCus * c.occ));
+      const float seq = rounds * (sps * c.alone * rate + c.edge);
+      const float work = blocks / kCus * sps * c.full * rate + c.edge;
+      const float bytes = blocks * sps * (float)(c.ta + c.tb) * 128.0f / 16e6f;
+      float us = seq > work ? seq : work;
+      us = us > bytes ? us : bytes;
+      if (splits > 1) us += 3.5f + splits * (0.1f + out * 8 / 7.5e6f);
+      if (best_us == 0.0f || us < best_us) {
+        best_us = us;
+        best.shape = s;
+        best.plan.nca = nca;
+        best.plan.nrb = nrb;
+        best.plan.splits = splits;
+        best.plan.sps = sps;
+      }
+    }
+  }
+  return best;
 }
 
-size_t part_bytes(int op, int in_type, int rows, int N, int K, int groups) {
-  if (op == kFwd && few_rows(rows, groups)) return 0;
-  const Choice c = choose(op, in_type, rows, N, K, groups);
-  if (c.plan.splits == 1) return 0;
-  const size_t out = op == kFwd ? (size_t)rows * N : (op == kDx ? (size_t)rows * K : (size_t)groups * N * K);
-  return out * c.plan.splits * sizeof(float);
+// The forward product of a few rows in all takes k_linear_few while the blocks
+// of groups with rows are no more than the compute units, and those of groups
+// without few enough to come and go (measured: one row, 4096 x 7168: 8.9 us
+// against 10.4 by tiles; 9 rows of 11 groups, 1140 x 752, up to 648 live blocks:
+// 12.3 us against 7.6).
+bool few_rows(int rows, int N, int groups) {
+  const long each = ceil_div(N, 16), live = rows < groups ? rows : groups;
+  return rows <= 16 && live * each <= kCus && groups * each <= 8 * kCus;
+}
+
+// Partial sums of any split that choose() may take for this product.
+size_t part_bytes(int op, int rows, int N, int K, int groups) {
+  const int cols = op == kFwd ? N : K;
+  const size_t one = (op == kDw ? (size_t)groups * N : (size_t)rows) * ((cols + 3) & ~3) * sizeof(float);
+  if (2 * one > kPartMax) return 0;
+  return one * kMaxSplits < kPartMax ? one * kMaxSplits : kPartMax;
 }
 
 template <class C>
@@ -773,28 +827,24 @@ hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   c.plan.out_type = out_type;
   p.part = ws;
   hipError_t e;
-  if (OP == kFwd && few_rows(p.rows, p.groups)) {
-    const int avg = ceil_div(p.rows, p.groups);
-    if (avg <= 16) k_linear_few<IN, 1, 1, 4><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
-    else k_linear_few<IN, 1, 2, 2><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
+  if (OP == kFwd && few_rows(p.rows, p.N, p.groups)) {
+    k_linear_few<IN, 1, 1, 4><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
     return hipGetLastError();
   }
   if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 1, 2, 1>>(p, c.plan, st);
   else if (c.shape == 1) e = run_shape<Shape<IN, OP, 256, 128, 4, 2, 1, 3, 1>>(p, c.plan, st);
-  else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 1, 3, 2>>(p, c.plan, st);
+  else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 1, 2, 2>>(p, c.plan, st);
+  else if (c.shape == 3) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 1, 3, 2>>(p, c.plan, st);
   else if (c.shape == 4) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 2, 3, 1>>(p, c.plan, st);
-  else if (c.shape == 5) e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 2, 3, 1>>(p, c.plan, st);
-  else if (c.shape == 6) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 1, 2, 2>>(p, c.plan, st);
-  else if (c.shape == 7) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 2, 2, 1>>(p, c.plan, st);
   else e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 1, 3, 2>>(p, c.plan, st);
   if (e != hipSuccess || c.plan.splits == 1) return e;
   const int cols = OP == kFwd ? p.N : p.K;
-  const size_t total = (OP == kDw ? (size_t)p.groups * p.N : (size_t)p.rows) * cols;
-  const size_t want = (cols % 4 == 0 ? total / 4 : total) / 256 + 1;
+  const int rows = OP == kDw ? p.groups * p.N : p.rows;  // a split output is at most kPartMax
+  const size_t want = ((size_t)rows * ceil_div(cols, 4) + 255) / 256;
   const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
-  if (out_type == kBF16) k_linear_join<kBF16><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
-  else if (out_type == kF16) k_linear_join<kF16><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
-  else k_linear_join<kF32><<<blocks, 256, 0, st>>>(p, total, cols, c.plan.splits, OP != kDw);
+  if (out_type == kBF16) k_linear_join<kBF16><<<blocks, 256, 0, st>>>(p, rows, cols, c.plan.splits, OP != kDw);
+  else if (out_type == kF16) k_linear_join<kF16><<<blocks, 256, 0, st>>>(p, rows, cols, c.plan.splits, OP != kDw);
+  else k_linear_join<kF32><<<blocks, 256, 0, st>>>(p, rows, cols, c.plan.splits, OP != kDw);
   return hipGetLastError();
 }
 
@@ -808,10 +858,10 @@ hipError_t run_in(int op, int out_type, const LinearArgs& p, void* ws, hipStream
 }  // namespace
 
 size_t linear_workspace(int rows, int N, int K, int groups, int in_type) {
-  size_t n = part_bytes(kFwd, in_type, rows, N, K, groups);
+  size_t n = part_bytes(kFwd, rows, N, K, groups);
   if (in_type != kFP8)
     for (int op = kDx; op <= kDw; ++op) {
-      const size_t m = part_bytes(op, in_type, rows, N, K, groups);
+      const size_t m = part_bytes(op, rows, N, K, groups);
       n = m > n ? m : n;
     }
   return n;

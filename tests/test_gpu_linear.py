@@ -409,6 +409,45 @@ def test_no_rows():
     mx.moe_fp8_quant(torch.empty(0, 128, device="cuda"), q, torch.empty(0, 1, device="cuda"))
 
 
+# Few tiles and a long reduction: it is split over blocks, whose partial sums a
+# second kernel joins.
+SPLIT = [(40, 1, 131, 6160), (77, 2, 257, 3088), (33, 3, 50, 7024)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,groups,N,K", SPLIT)
+def test_split_fp8(rows, groups, N, K, out):
+    _say(f"[case] split fp8 rows={rows} groups={groups} N={N} K={K} out={out}")
+    c = _fp8_case(_rng(17, rows, groups, N, K), rows, groups, N, K)
+    y = _run_fp8(*c, out=out)
+    ref, tol = ol.fp8_linear(_np(c[0].float()), c[1].astype(float), _np(c[2].float()), c[3].astype(float), c[4])
+    _check(_np(y), ref, tol, T[out])
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,groups,N,K", [(40, 2, 136, 4104), (40, 2, 4104, 136), (6000, 1, 64, 72), (5000, 2, 72, 64),
+                                             (60, 1, 72, 8200)])
+def test_split_grouped(rows, groups, N, K, out):
+    """Rows outside every group keep their values here too."""
+    _say(f"[case] split grouped rows={rows} groups={groups} N={N} K={K} out={out}")
+    rng = _rng(18, rows, groups, N, K)
+    x, w, dy, _ = _case16(rng, "bf16", rows, groups, N, K, ())
+    off = np.array([5, rows - 3] if groups == 1 else [5, rows // 3, rows - 3], np.int32)
+    d = mx.Linear(rows, N, K, groups=groups, out_type=out)
+    ws, do = mx.linear_workspace(d), _dev_off(off)
+    ws.fill_(0xFF)
+    y, dx = (torch.full((rows, n), 7.0, dtype=T[out], device="cuda") for n in (N, K))
+    dw = torch.full((groups, N, K), 7.0, dtype=T[out], device="cuda")
+    mx.moe_grouped_linear(d, x, w, y, ws, offsets=do)
+    mx.moe_grouped_linear_dx(d, dy, w, dx, ws, offsets=do)
+    mx.moe_grouped_linear_dw(d, dy, x, dw, ws, offsets=do)
+    torch.cuda.synchronize()
+    for got, (ref, tol) in ((y, ol.grouped(_np(x), _np(w), off)), (dx, ol.grouped_dx(_np(dy), _np(w), off))):
+        assert torch.all(got[:5] == 7.0) and torch.all(got[-3:] == 7.0)
+        _check(_np(got)[5:-3], ref[5:-3], tol[5:-3], T[out])
+    _check(_np(dw), *ol.grouped_dw(_np(dy), _np(x), groups, off), T[out])
+
+
 def test_offsets_outside_the_rows_touch_nothing_outside():
     """Offsets that break the contract are clamped: the launch stays inside
     the tensors (no value is promised), and rows past `rows` keep theirs."""
