@@ -440,6 +440,13 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
             sold[j] = snew[j];
             snew[j] = sc[4 * (wb * TJ * 16 + 16 * j + l16)];
           }
+          // the second team's stage past the end (all zeros) finds the next
+          // row's scales, which may be NaN
+          if (C::KS > 1 && s * C::KS + team >= s_n) {
+            wsc = 0.f;
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) snew[j] = 0.f;
+          }
         }
         if (v == D) {
 #pragma unroll

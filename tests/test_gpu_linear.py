@@ -283,6 +283,24 @@ def test_fp8_linear_keeps_other_groups_and_rows_apart():
     assert torch.all(torch.isnan(y[20:61]))
 
 
+@pytest.mark.parametrize("rows,N,K", [(512, 4096, 784), (100, 4096, 5136)])
+def test_fp8_scales_of_the_next_row_stay_out(rows, N, K):
+    """An odd number of blocks of 128 on sizes whose tiles take them two at a
+    time: the scale that follows a row's last one belongs to the next row."""
+    _say(f"[case] next row's scales rows={rows} N={N} K={K}")
+    rng = _rng(19, rows, N, K)
+    x, w = _int16(rng, rows, K), _int16(rng, N, K)
+    xs, ws = torch.ones(rows, ol.blocks(K), device="cuda"), torch.ones(1, ol.blocks(N), ol.blocks(K), device="cuda")
+    xs[1::2, 0], ws[0, 1::2, 0] = float("nan"), float("inf")
+    d = mx.Linear(rows, N, K, in_type="fp8", out_type="f32")
+    y = torch.full((rows, N), 0.5, device="cuda")
+    mx.moe_fp8_linear(d, x.to(torch.float8_e4m3fn), xs, w.to(torch.float8_e4m3fn), ws, y, mx.linear_workspace(d))
+    ref = (x.double() @ w.double().t()).float()
+    even = torch.arange(N, device="cuda") // 128 % 2 == 0
+    assert torch.equal(y[::2][:, even], ref[::2][:, even])
+    assert torch.all(torch.isnan(y[1::2]))
+
+
 # ---------------------------------------------------------------------------
 # 16-bit products by group
 # ---------------------------------------------------------------------------
