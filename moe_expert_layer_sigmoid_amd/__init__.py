@@ -531,9 +531,31 @@ def linear_workspace(d: Linear, device="cuda") -> torch.Tensor:
     return torch.empty(max(moe_linear_workspace_bytes(d), 256), dtype=u8, device=device)
 
 
-# The smallest linear calls take a few us on the GPU, so their host side is
-# kept short: one pass of checks per tensor, addresses as plain ints, the
-# current stream without a Stream object (measured: 10.0 -> 5.6 us a call of the quantiser).
+# The smallest linear calls take 2 to 5 us on the GPU, so their host side is
+# kept short: _bind (csrc/bind.cpp) checks the tensors and launches on the
+# current stream in one call.  Where it finds something else than it expects (an
+# explicit stream, another device, a tensor that does not fit) it launches
+# nothing and returns None; the checks below then run, and say what is wrong.
+# (A call of the quantiser, one row: 5.6 us with the checks in Python, 3.3 here,
+# of which the launch is 3.2.)
+
+_bind_module = None
+
+
+def _short():
+    global _bind_module
+    if _bind_module is None:
+        lib()
+        from . import _bind
+        _bind_module = _bind
+    return _bind_module
+
+
+def _device(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return t.get_device()
+
 
 def _addr(t: torch.Tensor, name: str, dtype, numel_min: int, dev: int) -> int:
     """The address of a tensor that fits; _refuse says why one does not."""
@@ -598,12 +620,20 @@ def moe_fp8_quant(x, q, qs, stream=None) -> None:
     """q (float8_e4m3fn or uint8 [rows, K]) and qs (float32 [rows,
     ceil(K/128)]) of x [rows, K] (bfloat16, float16 or float32; rows may be
     further apart than K elements)."""
-    _fp8_quant("moe_fp8_quant", x, q, qs, 1, stream)
+    rc = _short().quant(False, x, q, qs, stream)
+    if rc is None:
+        _fp8_quant("moe_fp8_quant", x, q, qs, 1, stream)
+    elif rc:
+        raise MoeError("moe_fp8_quant", rc)
 
 
 def moe_fp8_swiglu_quant(x, q, qs, stream=None) -> None:
     """The same of silu(gate) * up, x [rows, 2K] holding gate | up."""
-    _fp8_quant("moe_fp8_swiglu_quant", x, q, qs, 2, stream)
+    rc = _short().quant(True, x, q, qs, stream)
+    if rc is None:
+        _fp8_quant("moe_fp8_swiglu_quant", x, q, qs, 2, stream)
+    elif rc:
+        raise MoeError("moe_fp8_swiglu_quant", rc)
 
 
 def _offsets(d: Linear, offsets, dev):
@@ -619,7 +649,12 @@ def moe_fp8_linear(d: Linear, xq, xs, w, ws, y, scratch, offsets=None, stream=No
     and fp8 weights w [groups, N, K] with scales ws [groups, ceil(N/128),
     ceil(K/128)]; ``offsets`` int32 [groups + 1] on the device (None: one
     group of all rows)."""
-    dev = y.get_device()
+    rc = _short().fp8(d, xq, xs, w, ws, y, scratch, offsets, stream)
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        raise MoeError("moe_fp8_linear", rc)
+    dev = _device(y, "y")
     _launch("moe_fp8_linear", dev, stream, ctypes.byref(d),
             _addr(xq, "xq", torch.float8_e4m3fn, d.rows * d.K, dev), _addr(xs, "xs", f32, d.rows * _blocks(d.K), dev),
             _addr(w, "w", torch.float8_e4m3fn, d.groups * d.N * d.K, dev),
@@ -627,27 +662,42 @@ def moe_fp8_linear(d: Linear, xq, xs, w, ws, y, scratch, offsets=None, stream=No
             _addr(y, "y", _TORCH_TYPES[d.out_type], d.rows * d.N, dev), *_scratch(scratch, dev))
 
 
-def _grouped(fn, d: Linear, a, an, a_name, b, bn, b_name, out, on, out_name, scratch, offsets, stream) -> None:
-    dev = out.get_device()
+def _grouped(op, d: Linear, a, an, a_name, b, bn, b_name, out, on, out_name, scratch, offsets, stream) -> None:
+    fn = _GROUPED[op]
+    dev = _device(out, out_name)
     t = _TORCH_TYPES[d.in_type]
     _launch(fn, dev, stream, ctypes.byref(d), _addr(a, a_name, t, an, dev), _addr(b, b_name, t, bn, dev),
             _offsets(d, offsets, dev), _addr(out, out_name, _TORCH_TYPES[d.out_type], on, dev),
             *_scratch(scratch, dev))
 
 
+_GROUPED = ("moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw")
+
+
 def moe_grouped_linear(d: Linear, x, w, y, scratch, offsets=None, stream=None) -> None:
     """y [rows, N] = x [rows, K] times each group's w [N, K] transposed."""
-    _grouped("moe_grouped_linear", d, x, d.rows * d.K, "x", w, d.groups * d.N * d.K, "w", y, d.rows * d.N, "y",
-             scratch, offsets, stream)
+    rc = _short().grouped(0, d, x, w, y, scratch, offsets, stream)
+    if rc is None:
+        _grouped(0, d, x, d.rows * d.K, "x", w, d.groups * d.N * d.K, "w", y, d.rows * d.N, "y", scratch, offsets, stream)
+    elif rc:
+        raise MoeError("moe_grouped_linear", rc)
 
 
 def moe_grouped_linear_dx(d: Linear, dy, w, dx, scratch, offsets=None, stream=None) -> None:
     """dx [rows, K] = dy [rows, N] times each group's w [N, K]."""
-    _grouped("moe_grouped_linear_dx", d, dy, d.rows * d.N, "dy", w, d.groups * d.N * d.K, "w", dx, d.rows * d.K, "dx",
-             scratch, offsets, stream)
+    rc = _short().grouped(1, d, dy, w, dx, scratch, offsets, stream)
+    if rc is None:
+        _grouped(1, d, dy, d.rows * d.N, "dy", w, d.groups * d.N * d.K, "w", dx, d.rows * d.K, "dx", scratch, offsets,
+                 stream)
+    elif rc:
+        raise MoeError("moe_grouped_linear_dx", rc)
 
 
 def moe_grouped_linear_dw(d: Linear, dy, x, dw, scratch, offsets=None, stream=None) -> None:
     """dw [groups, N, K]: per group, dy [rows, N] transposed times x [rows, K]; zeros for an empty group."""
-    _grouped("moe_grouped_linear_dw", d, dy, d.rows * d.N, "dy", x, d.rows * d.K, "x", dw, d.groups * d.N * d.K, "dw",
-             scratch, offsets, stream)
+    rc = _short().grouped(2, d, dy, x, dw, scratch, offsets, stream)
+    if rc is None:
+        _grouped(2, d, dy, d.rows * d.N, "dy", x, d.rows * d.K, "x", dw, d.groups * d.N * d.K, "dw", scratch, offsets,
+                 stream)
+    elif rc:
+        raise MoeError("moe_grouped_linear_dw", rc)

@@ -173,3 +173,23 @@ def test_oracle_grouped_and_gradients():
         e = np.zeros_like(w)
         e[g, n, k] = 0.5
         assert abs(f(x, w + e) - f(x, w - e) - dw[g, n, k]) < 1e-10
+
+
+@needs_lib
+def test_binding_refuses_what_is_no_tensor_or_descriptor():
+    d = mx.Linear(2, 16, 16)
+    t = torch.zeros(2, 16).bfloat16()
+    for f in (mx.moe_grouped_linear, mx.moe_grouped_linear_dx, mx.moe_grouped_linear_dw):
+        with pytest.raises(TypeError):
+            f(d, t, t, None, None)
+        with pytest.raises((TypeError, ValueError)):
+            f(d, None, t, t, None)
+    with pytest.raises(TypeError):
+        mx.moe_fp8_linear(mx.Linear(2, 16, 16, in_type="fp8"), t, t, t, t, 5, None)
+    for f in (mx.moe_fp8_quant, mx.moe_fp8_swiglu_quant):
+        with pytest.raises(TypeError):
+            f(None, t, t)
+    bad = mx.Linear(2, 16, 16)
+    bad.in_type = 9
+    with pytest.raises((ValueError, IndexError)):
+        mx.moe_grouped_linear(bad, t, t, t, None)
