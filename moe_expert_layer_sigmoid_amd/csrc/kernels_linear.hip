@@ -68,49 +68,54 @@ __device__ __forceinline__ void group_rows(const int32_t* off, int g, int rows, 
   hi = off ? min(max(off[g + 1], lo), rows) : rows;
 }
 
-// The group that row tile `tile` (of TB rows, counted over the groups in
-// order) belongs to and its index there; false past the last one.  Every wave
-// does this by itself: 64 groups at a time, one per lane, prefix sums across
-// the lanes.
+// Row tiles of TB rows, counted over the groups in order.  Every wave does this
+// by itself: 64 groups at a time, one per lane, prefix sums across the lanes.
+// The first 64 groups' rows stay in registers, so that up to 64 groups cost one
+// trip to memory in all (three dependent ones, for the count, the search and the
+// group's rows, took 0.5 us longer).
 template <int TB>
-__device__ __forceinline__ bool find_tile(const int32_t* off, int groups, int rows, int tile, int& g, int& t) {
-  const int lane = threadIdx.x & 63;
-  int base = 0;
-  for (int c = 0; c < groups; c += 64) {
-    int lo = 0, hi = 0;
-    if (c + lane < groups) group_rows(off, c + lane, rows, lo, hi);
-    const int nt = (hi - lo + TB - 1) / TB;
-    int incl = nt;
+struct RowTiles {
+  const int32_t* off;
+  int groups, rows;
+  int lo, hi, incl;  // of group `lane`: its rows, and the tiles up to its end
+  int total;         // row tiles of all groups
+
+  __device__ __forceinline__ int load(int c, int base, int& lo_, int& hi_) const {  // of groups [c, c + 64)
+    const int lane = threadIdx.x & 63;
+    lo_ = hi_ = 0;
+    if (c + lane < groups) group_rows(off, c + lane, rows, lo_, hi_);
+    int n = (hi_ - lo_ + TB - 1) / TB;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(incl, d);
-      if (lane >= d) incl += up;
+      const int up = __shfl_up(n, d);
+      if (lane >= d) n += up;
     }
-    const unsigned long long past = __ballot(base + incl > tile);
-    if (past) {
-      const int l = __ffsll(past) - 1;
-      g = __builtin_amdgcn_readfirstlane(c + l);
-      t = __builtin_amdgcn_readfirstlane(tile - base - __shfl(incl - nt, l));
-      return true;
+    return n + base;
+  }
+  __device__ __forceinline__ RowTiles(const int32_t* off_, int groups_, int rows_) : off(off_), groups(groups_), rows(rows_) {
+    incl = load(0, 0, lo, hi);
+    total = __builtin_amdgcn_readlane(incl, 63);
+    for (int c = 64; c < groups; c += 64) {
+      int l, h;
+      total = __builtin_amdgcn_readlane(load(c, total, l, h), 63);
     }
-    base += __shfl(incl, 63);
   }
-  return false;
-}
-
-// Row tiles of all groups.
-template <int TB>
-__device__ __forceinline__ int count_tiles(const int32_t* off, int groups, int rows) {
-  int n = 0;
-  for (int c = threadIdx.x & 63; c < groups; c += 64) {
-    int lo, hi;
-    group_rows(off, c, rows, lo, hi);
-    n += (hi - lo + TB - 1) / TB;
+  // The group g of row tile `tile` < total, the tile's index t there, and the group's rows.
+  __device__ __forceinline__ void find(int tile, int& g, int& t, int& glo, int& ghi) const {
+    int c = 0, l = lo, h = hi, n = incl;
+    unsigned long long past = __ballot(n > tile);
+    while (!past && c + 64 < groups) {
+      c += 64;
+      n = load(c, __builtin_amdgcn_readlane(n, 63), l, h);
+      past = __ballot(n > tile);
+    }
+    const int k = past ? __ffsll(past) - 1 : 63;  // tile < total: there is one
+    g = c + k;
+    glo = __builtin_amdgcn_readlane(l, k);
+    ghi = __builtin_amdgcn_readlane(h, k);
+    t = tile - (__builtin_amdgcn_readlane(n, k) - (ghi - glo + TB - 1) / TB);
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-  return __builtin_amdgcn_readfirstlane(n);
-}
+};
 
 // Shape of a block's work.  TA x TB: columns x rows of its output tile; WA x WB
 // waves; KS: teams of that many waves, each with its own LDS ring and every
@@ -190,15 +195,15 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       nred = hi - lo;
       row0 = (size_t)g * p.N + r0;
     } else {
-      const int tiles = count_tiles<TB>(p.off, p.groups, p.rows) * pl.nca;
+      const RowTiles<TB> rt(p.off, p.groups, p.rows);
+      const int tiles = rt.total * pl.nca;
       const int items = tiles * pl.splits, share = (items + kXcd - 1) / kXcd;
       const int item = xcd * share + j;
       if (j >= share || item >= items) return;
       split = item / tiles;
       const int l0 = item - split * tiles;
       int t;
-      find_tile<TB>(p.off, p.groups, p.rows, l0 / pl.nca, g, t);
-      group_rows(p.off, g, p.rows, lo, hi);
+      rt.find(l0 / pl.nca, g, t, lo, hi);
       const int nrb = (hi - lo + TB - 1) / TB, l = t * pl.nca + l0 % pl.nca;
       const int band = l / (nrb * 4), rem = l - band * nrb * 4, w = min(4, pl.nca - 4 * band);
       r0 = lo + rem / w * TB;
