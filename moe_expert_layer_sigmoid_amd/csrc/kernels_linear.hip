@@ -40,6 +40,9 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) void* lds_void;
 
+template <int AUX>
+using Hint = std::integral_constant<int, AUX>;  // cache policy bits of a load: 2 = read once
+
 constexpr uint32_t kOob = 0x80000000u;  // a buffer offset past every buffer used here: the load gives zeros
 
 template <int IN>
@@ -158,6 +161,7 @@ struct Plan {
   int splits;    // ranges of the reduction, each by its own block into its own partial sums
   int sps;       // stages per split (kFwd, kDx; kDw divides each group's own stages)
   int out_type;
+  bool big;      // kFwd, kDx: the weights in use are more than kStreamMin bytes
 };
 
 template <class C>
@@ -177,6 +181,14 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   // on at one time read about 4 column and 8 row operands.
   int g, lo, hi, c0, r0, nr, nred, split;
   size_t row0;  // the tile's first row in the output
+  // Weights that leave the caches before they are needed again are loaded with
+  // the streaming policy (measured, us: 48 fp8 experts at 8 rows 233 -> 204, 48
+  // bf16 experts at 6144 uneven rows 645 -> 631; dx of 4 experts of 7168 x 2048
+  // at 4096 rows 163 -> 153).  Not where many row tiles share them (one expert
+  // of 8192 x 8192: dx 782 -> 799; forward with two row tiles sharing: 662 for
+  // the 645 above), nor where they stay in the memory-side cache (77 x 2041 x
+  // 7152 in fp8: 12.7 -> 16.5).
+  bool once = false;
   {
     const int xcd = blockIdx.x % kXcd, j = blockIdx.x / kXcd;
     if (OP == kDw) {
@@ -209,6 +221,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       r0 = lo + rem / w * TB;
       c0 = (4 * band + rem % w) * TA;
       nr = min(TB, hi - r0);
+      once = pl.big && nrb <= (OP == kDx ? 8 : 1);
       nred = OP == kFwd ? p.K : p.N;
       row0 = (size_t)r0;
     }
@@ -295,25 +308,25 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   // DMA instruction m of stage st into a ring slot.  Stages past the end load
   // nothing (their buffers have no bytes), so that every stage counts the
   // same number of loads.
-  auto dma = [&](lds_u8* wr, int st, int m, bool live) __attribute__((always_inline)) {
-    auto kc = [&](const uint8_t* base, uint32_t lim, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
+  auto dma = [&](auto aux, lds_u8* wr, int st, int m, bool live) __attribute__((always_inline)) {
+    auto kc = [&](auto hint, const uint8_t* base, uint32_t lim, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
       const uint32_t so = (uint32_t)st * 128u;
       const uint32_t v = so + kpc < rowb ? vo : kOob;  // pieces past the row's end
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(base, live ? lim : 0u), (lds_void)(dst + (wave + W * m) * 1024), 16,
-                                               v + (uint32_t)m * step, so, 0, 0);
+                                               v + (uint32_t)m * step, so, 0, decltype(hint)::value);
     };
-    auto mc = [&](const uint8_t* base, int ld, int col0, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
+    auto mc = [&](auto hint, const uint8_t* base, int ld, int col0, uint32_t vo, uint32_t step, int m, lds_u8* dst) {
       const int rows = live ? min(C::RE, nred - st * C::RE) : 0;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           make_rsrc(base + (size_t)st * C::RE * ld * 2, rows > 0 ? (uint32_t)(rows * ld - col0) * 2u : 0u),
-          (lds_void)(dst + (wave + W * m) * 1024), 16, vo + (uint32_t)m * step, 0, 0, 0);
+          (lds_void)(dst + (wave + W * m) * 1024), 16, vo + (uint32_t)m * step, 0, 0, decltype(hint)::value);
     };
     if (m < C::NA) {
-      if (C::AT) mc(abase, p.K, c0, avo, astep, m, wr);
-      else kc(abase, alim, avo, astep, m, wr);
+      if (C::AT) mc(aux, abase, p.K, c0, avo, astep, m, wr);
+      else kc(aux, abase, alim, avo, astep, m, wr);
     } else if (m < C::NA + C::NB) {
-      if (C::BT) mc(bbase, p.N, r0, bvo, bstep, m - C::NA, wr + TA * 128);
-      else kc(bbase, blim, bvo, bstep, m - C::NA, wr + TA * 128);
+      if (C::BT) mc(Hint<0>{}, bbase, p.N, r0, bvo, bstep, m - C::NA, wr + TA * 128);
+      else kc(Hint<0>{}, bbase, blim, bvo, bstep, m - C::NA, wr + TA * 128);
     }
   };
 
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   // From one barrier to the next: stage s's slot rd is complete, wr is free.
   // (swr, srd: the scales' buffers of the next and this group of four stages.)
   constexpr int kGroup = 4 / C::KS;  // this team's stages of a group
-  auto body = [&](lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, lds_u8* __restrict__ swr,
+  auto body = [&](auto aux, lds_u8* __restrict__ wr, const lds_u8* __restrict__ rd, lds_u8* __restrict__ swr,
                   const lds_u8* __restrict__ srd, int s) __attribute__((always_inline)) {
     const int k = (s + PRE) * C::KS + team, st = s_lo + k;
     const bool live = k < s_n;
@@ -428,14 +441,14 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
       if (scw && (s < 0 ? s == -PRE : s % kGroup == 0)) dma_scales(swr, s_lo + (s < 0 ? 0 : (s / kGroup + 1) * 4));
     if (s < 0) {
 #pragma unroll
-      for (int m = 0; m < C::NI; ++m) dma(wr, st, m, live);
+      for (int m = 0; m < C::NI; ++m) dma(aux, wr, st, m, live);
       return;
     }
 #pragma unroll
     for (int v = 0; v < U; ++v) {
 #pragma unroll
       for (int m = 0; m < C::NI; ++m)
-        if (m * C::P / C::NI == v) dma(wr, st, m, live);
+        if (m * C::P / C::NI == v) dma(aux, wr, st, m, live);
       if constexpr (IN == kFP8) {
         if (v == 0) {
           const lds_f32* sc = reinterpret_cast<const lds_f32*>(srd) + ((s * C::KS + team) & 3);
@@ -464,21 +477,25 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   lds_u8* const ring0 = (lds_u8*)ring + team * C::kTeam;
   lds_u8* const scale0 = ring0 + NS * C::kSlot;
   const int steps = (s_n + C::KS - 1) / C::KS;
-  int wslot = 0, rslot = 0;
-  for (int s = -PRE; s < steps; ++s) {
-    if (s >= 0) {
-      // this wave's part of stage s has landed (PRE - 1 younger stages may be
-      // in flight) and its reads of stage s - 1 are done; then the barrier
-      // says the same of every wave
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((PRE - 1) * C::NI) : "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+  auto run = [&](auto aux) __attribute__((always_inline)) {
+    int wslot = 0, rslot = 0;
+    for (int s = -PRE; s < steps; ++s) {
+      if (s >= 0) {
+        // this wave's part of stage s has landed (PRE - 1 younger stages may be
+        // in flight) and its reads of stage s - 1 are done; then the barrier
+        // says the same of every wave
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((PRE - 1) * C::NI) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
+      const int par = s < 0 ? 1 : (s / kGroup) & 1;  // the prologue's group goes into buffer 0
+      body(aux, ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, scale0 + (par ^ 1) * C::kScale, scale0 + par * C::kScale, s);
+      wslot = wslot == NS - 1 ? 0 : wslot + 1;
+      if (s >= 0) rslot = rslot == NS - 1 ? 0 : rslot + 1;
     }
-    const int par = s < 0 ? 1 : (s / kGroup) & 1;  // the prologue's group goes into buffer 0
-    body(ring0 + wslot * C::kSlot, ring0 + rslot * C::kSlot, scale0 + (par ^ 1) * C::kScale, scale0 + par * C::kScale, s);
-    wslot = wslot == NS - 1 ? 0 : wslot + 1;
-    if (s >= 0) rslot = rslot == NS - 1 ? 0 : rslot + 1;
-  }
+  };
+  if (OP != kDw && once) run(Hint<2>{});
+  else run(Hint<0>{});
   // the last stage's last steps
 #pragma unroll
   for (int j = 0; j < TJ; ++j) sold[j] = snew[j];
@@ -582,7 +599,9 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
 // One launch, no partial sums in memory, and columns / 16 TI blocks a group.
 constexpr int kFewWaves = 8;
 
-template <int IN, int TI, int TJ, int CH>
+// NT: the weights with the streaming policy (one row, 4096 x 7168 in fp8, cached:
+// 9.5 us with it, 8.3 without).
+template <int IN, int TI, int TJ, int CH, bool NT>
 __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int out_type) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int ES = IN == kFP8 ? 1 : 2;
@@ -623,7 +642,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
         const bool in = o + 64u * h < rowb;
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-          x.a[i][h] = buf_load16_p<2>(Ar, in ? (uint32_t)(16 * i + l16) * rowb + o + 64u * h : kOob, 0);
+          x.a[i][h] = buf_load16_p<NT ? 2 : 0>(Ar, in ? (uint32_t)(16 * i + l16) * rowb + o + 64u * h : kOob, 0);
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
           x.b[j][h] = buf_load16(Br, in ? (uint32_t)(16 * j + l16) * rowb + o + 64u * h : kOob, 0);
@@ -726,6 +745,7 @@ __global__ void __launch_bounds__(256) k_linear_join(LinearArgs p, int rows, int
 constexpr int kMaxSplits = 16;
 constexpr size_t kPartMax = (size_t)64 << 20;  // partial sums of a split reduction, at most
 constexpr int kCus = 256;
+constexpr size_t kStreamMin = (size_t)100 << 20;  // weights larger than this do not stay cached from call to call
 
 // Block shapes, and what each measured (us; fp8 at 8192 x 4096 x 7168 and 512 x
 // 4096 x 7168, 16-bit within a fifth of it): a stage of a block that has its
@@ -837,10 +857,13 @@ template <int IN, int OP>
 hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   Choice c = choose(OP, IN, p.rows, p.N, p.K, p.groups);
   c.plan.out_type = out_type;
+  c.plan.big = (size_t)(p.rows < p.groups ? p.rows : p.groups) * p.N * p.K * (IN == kFP8 ? 1 : 2) > kStreamMin;
   p.part = ws;
   hipError_t e;
   if (OP == kFwd && few_rows(p.rows, p.N, p.groups)) {
-    k_linear_few<IN, 1, 1, 4><<<dim3((unsigned)ceil_div(p.N, 16), p.groups), kFewWaves * 64, 0, st>>>(p, out_type);
+    const dim3 grid((unsigned)ceil_div(p.N, 16), p.groups);
+    if (c.plan.big) k_linear_few<IN, 1, 1, 4, true><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
+    else k_linear_few<IN, 1, 1, 4, false><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
     return hipGetLastError();
   }
   if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 1, 2, 1>>(p, c.plan, st);
