@@ -148,6 +148,7 @@ struct Shape {
   static constexpr int kLag = TJ == 1 ? 2 : 3;
   static_assert(U % 4 == 0 && D < 4 && kLag < 4 && (IN != kFP8 || kLag <= (U - D) * TJ), "rings of four");
   static_assert(NA * W * 8 == TA && NB * W * 8 == TB && TI * WA * 16 == TA && TJ * WB * 16 == TB, "tile shape");
+  static_assert((!AT || (TA & (TA - 1)) == 0) && (!BT || (TB & (TB - 1)) == 0), "transposed rows are permuted in powers of two");
   static_assert(PRE * NI + 1 < 64, "vmcnt range");
   static_assert(IN != kFP8 || TB / 64 < W, "a wave for the weight scales");
   static_assert(KS * kTeam <= 160 * 1024, "LDS");
@@ -531,16 +532,17 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
   }
 
   // ---- the tile's values, rounded once to the output type.  Each wave turns
-  // its 16-row strips in LDS (its share of the ring, two strips in turn), so
+  // its 16-row strips in LDS (its share of the ring, two strips in turn where they fit), so
   // that a store writes whole rows of the wave's columns.  (A lane's own 4 to
   // 16 consecutive columns stored directly: 8192 x 4096 x 7168 in fp8 215 us
   // against 205, the weight gradients of 4 experts of 7168 x 2048 157 against 128.)
   __syncthreads();
   constexpr int CW = TI * 16;               // the wave's columns
   constexpr int kStrip = 16 * CW * 4;
-  static_assert(2 * kStrip * W <= NS * C::kSlot, "strips fit the ring");
+  constexpr int kStrips = 2 * kStrip * W <= NS * C::kSlot ? 2 : 1;
+  static_assert(kStrips * kStrip * W <= NS * C::kSlot, "strips fit the ring");
   typedef __attribute__((address_space(3))) v4f lds_v4f;
-  lds_u8* const strip0 = (lds_u8*)ring + wave * 2 * kStrip;
+  lds_u8* const strip0 = (lds_u8*)ring + wave * kStrips * kStrip;
   auto write = [&](auto outc, void* out, int pitch) {
     constexpr int OUT = decltype(outc)::value;
     using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
     constexpr int LR = CW / V, RI = 64 / LR;  // lanes a row, rows an instruction
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      lds_u8* const strip = strip0 + (j & 1) * kStrip;
+      lds_u8* const strip = strip0 + j % kStrips * kStrip;
       // 16-byte chunk c of row r lies at chunk c ^ r: no two rows on one bank
 #pragma unroll
       for (int i = 0; i < TI; ++i)
@@ -747,23 +749,29 @@ constexpr size_t kPartMax = (size_t)64 << 20;  // partial sums of a split reduct
 constexpr int kCus = 256;
 constexpr size_t kStreamMin = (size_t)100 << 20;  // weights larger than this do not stay cached from call to call
 
-// Block shapes, and what each measured (us; fp8 at 8192 x 4096 x 7168 and 512 x
-// 4096 x 7168, 16-bit within a fifth of it): a stage of a block that has its
-// compute unit to itself on a half-empty card (`alone`), a stage per compute
-// unit with every one full (`full`), and a block's start and end (`edge`).
+// Block shapes and their costs (us, but for the factor of a product's kind
+// below): a stage of a block that has its compute unit to itself on a half-empty
+// card (`alone`), a stage per compute unit with every one full (`full`), and a
+// block's start and end (`edge`).  These and the constants of choose() are
+// fitted to the times of every shape and split on 680 products (170 random
+// sizes, 17 to 8192 rows, 1 to 48 groups, widths 128 to 8192).
 struct Cost {
   int ta, tb, occ;
   float alone, full, edge;
 };
-constexpr int kShapes = 6;
+constexpr int kShapes = 7;
 constexpr Cost kCost[kShapes] = {
-    {256, 256, 1, 1.15f, 1.73f, 8.0f},    // most arithmetic per byte moved: large products
-    {256, 128, 1, 0.72f, 1.00f, 5.0f},    // groups of about 100 rows: the weights pass through LDS once
-    {128, 128, 2, 0.70f, 0.545f, 4.0f},   // two blocks a compute unit: one stores while the other computes
-    {128, 64, 2, 0.46f, 0.32f, 2.6f},     // fewer rows a group
-    {128, 64, 1, 0.375f, 0.37f, 2.9f},    // the same by two teams: few tiles, a long reduction
-    {128, 32, 2, 0.38f, 0.265f, 2.0f},    // decode: the stream of the weights
+    {256, 256, 1, 1.19f, 1.51f, 6.6f},    // most arithmetic per byte moved: large products
+    {256, 128, 1, 0.73f, 0.88f, 4.2f},    // groups of about 100 rows: the weights pass through LDS once
+    {128, 128, 2, 0.73f, 0.78f, 3.5f},    // two blocks a compute unit: one stores while the other computes
+    {128, 64, 2, 0.59f, 0.38f, 3.1f},     // fewer rows a group
+    {128, 64, 1, 0.30f, 0.46f, 2.4f},     // the same by two teams: few tiles, a long reduction
+    {128, 32, 2, 0.29f, 0.33f, 1.8f},     // decode: the stream of the weights
+    {256, 192, 1, 1.00f, 1.08f, 6.5f},    // where 256 x 256 leaves compute units idle in its last round
 };
+// Factors of `alone` and `full`: 16-bit forward, dx, dw, fp8 forward.
+constexpr float kAlone[4] = {1.22f, 0.80f, 0.88f, 1.15f};
+constexpr float kFull[4] = {1.01f, 0.74f, 0.53f, 1.12f};
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -774,21 +782,23 @@ struct Choice {
 
 // The shape and the number of splits with the smallest estimate of
 //   max(rounds of blocks in sequence, the work at the full card's rate, the
-//   staged bytes at 16 TB/s) + the join of the splits.
+//   staged bytes at 14.8 TB/s) + the join of the splits.
 // The groups' sizes are on the device; the estimate takes them as equal, with
-// half a tile of waste each.  (Against timing every shape on the 105 products of
-// three sets of sizes the choice is 4.5 % from the best on average.)
+// half a tile of waste each.  (On 120 products that the fit has not seen the
+// choice is 1.6 % from the best on average, 21 % at worst.)
 Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
   const int re = in_type == kFP8 ? 128 : 64;
   const int cols = op == kFwd ? N : K;
   const int live = op == kDw ? groups : (rows < groups ? rows : groups);  // groups with rows, at most
   const int nst = ceil_div(op == kFwd ? K : (op == kDx ? N : ceil_div(rows, groups)), re);
-  const float rate = in_type == kFP8 ? 1.0f : 0.85f;
+  const int kind = in_type == kFP8 ? 3 : op;
+  const float alone = kAlone[kind], full = kFull[kind];
   const float out = (op == kDw ? (float)groups * N : (float)rows) * ((cols + 3) & ~3);
   Choice best{};
   float best_us = 0.0f;
   for (int s = 0; s < kShapes; ++s) {
     const Cost& c = kCost[s];
+    if (op == kDw && (c.tb & (c.tb - 1))) continue;  // its rows are read transposed: powers of two
     const int nca = ceil_div(cols, c.ta);
     int nrb;      // row tiles a group (kDw) or at most in all
     float tiles;  // expected in all
@@ -807,12 +817,12 @@ Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
       const int sps = ceil_div(nst > 0 ? nst : 1, want);
       const int splits = op == kDw ? want : ceil_div(nst > 0 ? nst : 1, sps);
       const float blocks = tiles * splits, rounds = ceilf(blocks / (kCus * c.occ));
-      const float seq = rounds * (sps * c.alone * rate + c.edge);
-      const float work = blocks / kCus * sps * c.full * rate + c.edge;
-      const float bytes = blocks * sps * (float)(c.ta + c.tb) * 128.0f / 16e6f;
+      const float seq = rounds * (sps * c.alone * alone + c.edge);
+      const float work = blocks / kCus * sps * c.full * full + c.edge;
+      const float bytes = blocks * sps * (float)(c.ta + c.tb) * 128.0f / 14.8e6f;
       float us = seq > work ? seq : work;
       us = us > bytes ? us : bytes;
-      if (splits > 1) us += 3.5f + splits * (0.1f + out * 8 / 7.5e6f);
+      if (splits > 1) us += 3.8f + splits * (0.14f + out * 8 / 6.9e6f);
       if (best_us == 0.0f || us < best_us) {
         best_us = us;
         best.shape = s;
@@ -871,7 +881,9 @@ hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 1, 2, 2>>(p, c.plan, st);
   else if (c.shape == 3) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 1, 3, 2>>(p, c.plan, st);
   else if (c.shape == 4) e = run_shape<Shape<IN, OP, 128, 64, 2, 2, 2, 3, 1>>(p, c.plan, st);
-  else e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 1, 3, 2>>(p, c.plan, st);
+  else if (c.shape == 5) e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 1, 3, 2>>(p, c.plan, st);
+  else if constexpr (OP != kDw) e = run_shape<Shape<IN, OP, 256, 192, 2, 4, 1, 2, 1>>(p, c.plan, st);
+  else return hipErrorInvalidValue;  // choose() does not take it for kDw
   if (e != hipSuccess || c.plan.splits == 1) return e;
   const int cols = OP == kFwd ? p.N : p.K;
   const int rows = OP == kDw ? p.groups * p.N : p.rows;  // a split output is at most kPartMax

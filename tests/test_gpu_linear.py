@@ -264,6 +264,20 @@ def test_large_tiles_exact_on_small_integers(rows, groups, N, K):
             assert torch.equal(got, r), (dt, name)
 
 
+# For each product, sizes at which each of the block shapes is the one chosen.
+SHAPES = [
+    (2779, 3, 4376, 80), (2658, 12, 1976, 80), (2694, 5, 1464, 80), (2367, 1, 824, 80), (4475, 2, 272, 272),
+    (135, 1, 136, 80), (4727, 5, 1648, 80), (2382, 12, 120, 3952), (3326, 1, 104, 2016), (3779, 3, 120, 1040),
+    (2299, 5, 112, 832), (2708, 2, 112, 3424), (103, 30, 224, 1072), (311, 1, 2000, 3856), (144, 30, 1248, 80),
+    (106, 30, 552, 80), (5383, 12, 632, 144), (471, 30, 1096, 144), (948, 12, 4840, 80), (5716, 3, 192, 416),
+    (5893, 1, 1440, 80), (2500, 1, 4104, 1040)]
+
+
+@pytest.mark.parametrize("rows,groups,N,K", SHAPES)
+def test_every_shape_exact_on_small_integers(rows, groups, N, K):
+    test_large_tiles_exact_on_small_integers(rows, groups, N, K)
+
+
 def test_fp8_linear_keeps_other_groups_and_rows_apart():
     """NaN codes and scales in one group's rows and weights reach that group's
     outputs alone; rows in no group are not written."""
