@@ -753,25 +753,25 @@ constexpr size_t kStreamMin = (size_t)100 << 20;  // weights larger than this do
 // below): a stage of a block that has its compute unit to itself on a half-empty
 // card (`alone`), a stage per compute unit with every one full (`full`), and a
 // block's start and end (`edge`).  These and the constants of choose() are
-// fitted to the times of every shape and split on 680 products (170 random
-// sizes, 17 to 8192 rows, 1 to 48 groups, widths 128 to 8192).
+// fitted to the times of every shape and split on 1040 products (260 random
+// sizes, 1 to 8192 rows, 1 to 48 groups, widths 64 to 8192).
 struct Cost {
   int ta, tb, occ;
   float alone, full, edge;
 };
 constexpr int kShapes = 7;
 constexpr Cost kCost[kShapes] = {
-    {256, 256, 1, 1.19f, 1.51f, 6.6f},    // most arithmetic per byte moved: large products
-    {256, 128, 1, 0.73f, 0.88f, 4.2f},    // groups of about 100 rows: the weights pass through LDS once
-    {128, 128, 2, 0.73f, 0.78f, 3.5f},    // two blocks a compute unit: one stores while the other computes
-    {128, 64, 2, 0.59f, 0.38f, 3.1f},     // fewer rows a group
-    {128, 64, 1, 0.30f, 0.46f, 2.4f},     // the same by two teams: few tiles, a long reduction
-    {128, 32, 2, 0.29f, 0.33f, 1.8f},     // decode: the stream of the weights
-    {256, 192, 1, 1.00f, 1.08f, 6.5f},    // where 256 x 256 leaves compute units idle in its last round
+    {256, 256, 1, 1.25f, 1.39f, 6.6f},    // most arithmetic per byte moved: large products
+    {256, 128, 1, 0.75f, 0.855f, 4.3f},   // groups of about 100 rows: the weights pass through LDS once
+    {128, 128, 2, 0.77f, 0.785f, 3.5f},   // two blocks a compute unit: one stores while the other computes
+    {128, 64, 2, 0.63f, 0.38f, 2.9f},     // fewer rows a group
+    {128, 64, 1, 0.30f, 0.43f, 2.6f},     // the same by two teams: few tiles, a long reduction
+    {128, 32, 2, 0.285f, 0.415f, 1.6f},  // decode: the stream of the weights
+    {256, 192, 1, 1.00f, 1.19f, 5.3f},    // where 256 x 256 leaves compute units idle in its last round
 };
 // Factors of `alone` and `full`: 16-bit forward, dx, dw, fp8 forward.
-constexpr float kAlone[4] = {1.22f, 0.80f, 0.88f, 1.15f};
-constexpr float kFull[4] = {1.01f, 0.74f, 0.53f, 1.12f};
+constexpr float kAlone[4] = {0.99f, 0.80f, 0.92f, 1.15f};
+constexpr float kFull[4] = {1.09f, 0.80f, 0.39f, 1.12f};
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -784,8 +784,8 @@ struct Choice {
 //   max(rounds of blocks in sequence, the work at the full card's rate, the
 //   staged bytes at 14.8 TB/s) + the join of the splits.
 // The groups' sizes are on the device; the estimate takes them as equal, with
-// half a tile of waste each.  (On 120 products that the fit has not seen the
-// choice is 1.6 % from the best on average, 21 % at worst.)
+// half a tile of waste each.  (On these and 280 further products the
+// choice is 2.0 % from the best on average.)
 Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
   const int re = in_type == kFP8 ? 128 : 64;
   const int cols = op == kFwd ? N : K;
@@ -822,7 +822,7 @@ Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
       const float bytes = blocks * sps * (float)(c.ta + c.tb) * 128.0f / 14.8e6f;
       float us = seq > work ? seq : work;
       us = us > bytes ? us : bytes;
-      if (splits > 1) us += 3.8f + splits * (0.14f + out * 8 / 6.9e6f);
+      if (splits > 1) us += 2.9f + splits * (0.17f + out * 8 / 6.5e6f);
       if (best_us == 0.0f || us < best_us) {
         best_us = us;
         best.shape = s;
