@@ -8,10 +8,15 @@
 //   y[row, n]   : A = w  [n][k],  B = x [row][k],   reduced over k
 //   dx[row, k]  : A = w  [n][k]^T, B = dy [row][n], reduced over n
 //   dw[n, k]    : A = x  [row][k]^T, B = dy [row][n]^T, reduced over rows
-// An operand whose reduction is not contiguous is transposed on its way into
-// LDS.  fp8: the four scales of a 128-column stage are constant over it, so
+// An operand whose reduction is not contiguous is read from LDS with the
+// transposing load.  fp8: the scales of a 128-column stage are constant over it, so
 // one 16x16x128 product per tile is scaled by xs * ws in f32 and added to an
 // f32 accumulator.
+//
+// Bound by the staging into LDS nearly everywhere (us, and with the products
+// left out): fp8 8192 x 4096 x 7168 207 (2.3 PFLOP/s) and 182; 48 fp8 experts at
+// 6144 rows 191 and 183; 48 bf16 experts 630 and 630 (5 TB/s past L2); 512 fp8
+// rows 23 and 21.  With few rows an expert the weights stream at 6.9 TB/s.
 
 #include <hip/hip_runtime.h>
 
@@ -838,7 +843,7 @@ Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
 
 // The forward product of a few rows in all takes k_linear_few while the blocks
 // of groups with rows are no more than the compute units, and those of groups
-// without few enough to come and go (measured: one row, 4096 x 7168: 8.9 us
+// without few enough to come and go (measured: one row, 4096 x 7168: 8.3 us
 // against 10.4 by tiles; 9 rows of 11 groups, 1140 x 752, up to 648 live blocks:
 // 12.3 us against 7.6).
 bool few_rows(int rows, int N, int groups) {
