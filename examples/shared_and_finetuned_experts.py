@@ -149,8 +149,8 @@ def main() -> None:
         err = y - target
         _, _, dw1, dw2 = finetune_step(b.x, w, tokens, offsets, w1, w2, err.bfloat16())
         print(f"step {step}: loss {float(0.5 * err.square().sum()):.6g}")
-        w1 = (w1.float() - 0.05 * dw1).bfloat16()
-        w2 = (w2.float() - 0.05 * dw2).bfloat16()
+        w1 = (w1.float() - 0.01 * dw1).bfloat16()
+        w2 = (w2.float() - 0.01 * dw2).bfloat16()
 
 
 if __name__ == "__main__":
