@@ -424,7 +424,9 @@ size_t moe_linear_workspace_bytes(const moe_linear_t* d);
 int moe_fp8_quant(int32_t rows, int32_t K, int32_t x_type, const void* x, int64_t ldx, uint8_t* q, float* qs,
                   moe_stream_t stream);
 
-/* The same of h = silu(x[:, :K]) * x[:, K:2K] in f32; x [rows, 2K], ldx >= 2K. */
+/* The same of h = silu(x[:, :K]) * x[:, K:2K] in f32; x [rows, 2K], ldx >= 2K.
+ * h keeps its value where silu alone leaves f32's normal range (gates below
+ * -87) and a large x[:, K:2K] brings the product back. */
 int moe_fp8_swiglu_quant(int32_t rows, int32_t K, int32_t x_type, const void* x, int64_t ldx, uint8_t* q, float* qs,
                          moe_stream_t stream);
 

@@ -2,8 +2,9 @@
 // behind SwiGLU:
 //   s = max(amax |v| / 448, 2^-126),  q = e4m3_rne(v * (1 / s)),
 // v = x, or silu(gate) * up in f32.  The division, the reciprocal and the
-// product are correctly rounded f32, so the codes are those of the same
-// formula evaluated anywhere in f32.  The floor 2^-126 keeps 1 / s finite for
+// product are correctly rounded f32, so the codes of the plain form are those of
+// the same formula evaluated anywhere in f32 (silu's exponential and reciprocal
+// are the hardware's; see silu_mul).  The floor 2^-126 keeps 1 / s finite for
 // blocks of zeros.  A block holding a NaN or an infinity gets a scale that is
 // NaN or infinite, as the formula says (amax is taken with NaN kept).
 
@@ -57,14 +58,26 @@ __device__ __forceinline__ float exp_neg(float g) {
   return __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.69314718f, 1.0f);
 }
 
-// silu(g) u: the hardware's reciprocal (1 ulp) in place of a division keeps
-// the kernel on the memory's side of its balance (in all within 8 x 2^-24 of
-// the value, far below the codes' 2^-4).  Beyond +-88 e^-g is 0 or infinite in
-// f32 and the sigmoid 1 or 0 (g = -inf: NaN, as in the formula).
+// silu(g) u for g >= kFarGate: the hardware's reciprocal (1 ulp) in place of a
+// division keeps the kernel on the memory's side of its balance (in all within
+// 9 x 2^-24 of the value, far below the codes' 2^-4).  Above 88 the sigmoid
+// rounds to 1, and e^-inf by the two parts above would be NaN.
+constexpr float kFarGate = -80.0f;
 __device__ __forceinline__ float silu_mul(float g, float u) {
   const float e = exp_neg(g);
-  const float r = g < -88.0f ? 0.0f : (g > 88.0f ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e));
+  const float r = g > 88.0f ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e);
   return g * r * u;
+}
+
+// silu(g) u for g < kFarGate, where 1 + e^-g rounds to e^-g: g e^g u.  Below
+// -87 neither e^g nor its reciprocal is a normal f32, while the product may be
+// one (silu(-88) = -5e-37, times u): t = e^(g/4) is normal down to -349, where
+// no u brings the product back into range, and every partial product is
+// normal wherever the result is (four errors of t and five roundings: 21 x
+// 2^-24).  g = -inf: NaN, as in the formula.
+__device__ __forceinline__ float silu_mul_far(float g, float u) {
+  const float t = exp_neg(-0.25f * g);
+  return (g * t) * (u * t) * t * t;
 }
 
 // One thread per 16 columns, 8 threads per block of 128: every load and store
@@ -85,8 +98,19 @@ __global__ void __launch_bounds__(kQuantThreads)
     if constexpr (SWIGLU) {
       float u[kPer];
       load_row<XT>(x, row * ldx + K + c, u);
+      float g[kPer];
+      bool far = false;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = silu_mul(v[i], u[i]);
+      for (int i = 0; i < kPer; ++i) {
+        g[i] = v[i];
+        far |= g[i] < kFarGate;
+        v[i] = silu_mul(g[i], u[i]);
+      }
+      if (far) {  // one branch for all columns: no trained model's gates get there
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (g[i] < kFarGate) v[i] = silu_mul_far(g[i], u[i]);
+      }
     }
   }
   // as bits: magnitudes order like integers, infinity above them, NaN above all
