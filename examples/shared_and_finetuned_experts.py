@@ -35,15 +35,15 @@ def to_fp8_blocks(w: torch.Tensor):
 
 
 class SharedExpert:
-    """down(silu(gate(x)) * up(x)) in fp8 for up to ``rows`` rows of bf16."""
+    """down(silu(gate(x)) * up(x)) in fp8 for up to ``rows`` rows of bf16; the
+    result is a view of a buffer that the next call overwrites."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, rows: int):
         H, F = down.shape
         dev = gate_up.device
+        self.rows, self.H, self.F = rows, H, F
         self.w1, self.w1s = to_fp8_blocks(gate_up)   # [2F, H]
         self.w2, self.w2s = to_fp8_blocks(down)      # [H, F]
-        self.d1 = mx.Linear(rows, 2 * F, H, in_type="fp8")
-        self.d2 = mx.Linear(rows, H, F, in_type="fp8")
         n = lambda w: -(-w // BLOCK)  # noqa: E731
         self.xq = torch.empty(rows, H, dtype=torch.float8_e4m3fn, device=dev)
         self.xs = torch.empty(rows, n(H), device=dev)
@@ -51,15 +51,24 @@ class SharedExpert:
         self.aq = torch.empty(rows, F, dtype=torch.float8_e4m3fn, device=dev)
         self.asc = torch.empty(rows, n(F), device=dev)
         self.y = torch.empty(rows, H, dtype=torch.bfloat16, device=dev)
-        self.scratch = torch.empty(max(mx.moe_linear_workspace_bytes(self.d1), mx.moe_linear_workspace_bytes(self.d2), 256),
-                                   dtype=torch.uint8, device=dev)
+        # enough for any number of rows up to `rows`: fewer may need more
+        need = max(mx.moe_linear_workspace_bytes(d) for r in range(1, rows + 1) for d in self._products(r))
+        self.scratch = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
+    def _products(self, r: int):
+        return mx.Linear(r, 2 * self.F, self.H, in_type="fp8"), mx.Linear(r, self.H, self.F, in_type="fp8")
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
-        mx.moe_fp8_quant(x, self.xq, self.xs)
-        mx.moe_fp8_linear(self.d1, self.xq, self.xs, self.w1, self.w1s, self.h, self.scratch)
-        mx.moe_fp8_swiglu_quant(self.h, self.aq, self.asc)
-        mx.moe_fp8_linear(self.d2, self.aq, self.asc, self.w2, self.w2s, self.y, self.scratch)
-        return self.y
+        r = x.shape[0]
+        if r > self.rows:
+            raise ValueError(f"{r} rows, made for at most {self.rows}")
+        d1, d2 = self._products(r)
+        xq, xs, h, aq, asc, y = (t[:r] for t in (self.xq, self.xs, self.h, self.aq, self.asc, self.y))
+        mx.moe_fp8_quant(x, xq, xs)
+        mx.moe_fp8_linear(d1, xq, xs, self.w1, self.w1s, h, self.scratch)
+        mx.moe_fp8_swiglu_quant(h, aq, asc)
+        mx.moe_fp8_linear(d2, aq, asc, self.w2, self.w2s, y, self.scratch)
+        return y
 
 
 class Buffers:

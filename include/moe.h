@@ -412,7 +412,8 @@ typedef struct {
 } moe_linear_t;
 
 /* Workspace bytes of any linear call on these sizes, the gradients included
- * (independent of out_type).  May be 0; returns 0 for invalid sizes too. */
+ * (independent of out_type).  May be 0; returns 0 for invalid sizes too.  It is
+ * no bound for fewer rows, which may need more: split reductions are for few. */
 size_t moe_linear_workspace_bytes(const moe_linear_t* d);
 
 /* q u8 [rows, K] = e4m3_rne(x * (1 / s)), qs f32 [rows, ceil(K/128)]:
