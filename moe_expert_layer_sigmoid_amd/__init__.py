@@ -78,6 +78,9 @@ class Linear(ctypes.Structure):
         for n, t in (("in_type", in_type), ("out_type", out_type)):
             if t not in TYPES:
                 raise ValueError(f"{n}: {t!r} is none of {', '.join(TYPES)}")
+        for n, v in (("rows", rows), ("N", N), ("K", K), ("groups", groups)):   # ctypes would keep the low 32 bits
+            if not -2 ** 31 <= int(v) < 2 ** 31:
+                raise ValueError(f"{n}: {v} is no 32-bit integer")
         super().__init__(int(rows), int(N), int(K), int(groups), TYPES[in_type], TYPES[out_type])
 
 
