@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Dict, Optional
 
 import torch
@@ -542,15 +543,31 @@ def linear_workspace(d: Linear, device="cuda") -> torch.Tensor:
 # (A call of the quantiser, one row: 5.6 us with the checks in Python, 3.3 here,
 # of which the launch is 3.2.)
 
+# Where _bind is missing or was built for another torch, every call takes the
+# checks in Python: the same kernels, 2 us more a call.
+
 _bind_module = None
+
+
+class _PythonChecks:
+    """In place of _bind: launches nothing."""
+    quant = fp8 = grouped = staticmethod(lambda *a: None)
 
 
 def _short():
     global _bind_module
     if _bind_module is None:
         lib()
-        from . import _bind
-        _bind_module = _bind
+        try:
+            from . import _bind
+            built = getattr(_bind, "torch_version", "of unknown version")
+            if built != str(torch.__version__):
+                raise ImportError(f"it was built for torch {built}, this is {torch.__version__}")
+            _bind_module = _bind
+        except ImportError as e:
+            warnings.warn(f"linear calls take longer on the host, _bind cannot be used: {e}; build it with "
+                          "`python -m moe_expert_layer_sigmoid_amd.build`", RuntimeWarning, stacklevel=3)
+            _bind_module = _PythonChecks
     return _bind_module
 
 

@@ -57,9 +57,11 @@ def _build_bind(verbose: bool) -> None:
     inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include"), os.path.join(ROOT, "include")]
     tmp = BIND + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(a for p in inc for a in ("-isystem", p)),
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f'-DMOE_TORCH_VERSION="{torch.__version__}"', *(a for p in inc for a in ("-isystem", p)),
           os.path.join(CSRC, "bind.cpp"), "-o", tmp, LIB, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu",
-          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose, "bind.cpp")
+          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose,
+         "bind.cpp (libmoe.so is built and complete: without _bind the linear calls are checked in Python)")
     os.replace(tmp, BIND)
 
 

@@ -23,7 +23,8 @@ constexpr at::ScalarType kTypes[] = {at::kBFloat16, at::kHalf, at::kFloat, at::k
 
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
-// A plain device tensor (no subclass that only pretends to have storage).
+// A device tensor.  (data_ptr() throws for a subclass without storage of its own;
+// the caller then takes the checks in Python.)
 const at::Tensor* tensor(PyObject* o) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
@@ -172,4 +173,10 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&kModule); }
+// torch_version: the torch whose headers and libraries this was built against.
+// Nothing here touches a tensor before the caller has compared it.
+PyMODINIT_FUNC PyInit__bind() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "torch_version", MOE_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
