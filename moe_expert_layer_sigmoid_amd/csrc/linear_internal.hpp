@@ -5,16 +5,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "linear_plan.hpp"
+
 namespace moe {
-
-// moe_dtype_t of include/moe.h
-enum { kBF16 = 0, kF16 = 1, kF32 = 2, kFP8 = 3 };
-
-// What a product computes; "columns" are the output's contiguous dimension.
-//  kFwd: y[row, n]  = sum_k x[row, k] w[g, n, k]
-//  kDx:  dx[row, k] = sum_n dy[row, n] w[g, n, k]
-//  kDw:  dw[g, n, k] = sum over the group's rows of dy[row, n] x[row, k]
-enum { kFwd = 0, kDx = 1, kDw = 2 };
 
 struct LinearArgs {
   const void* a;       // columns' operand: kFwd, kDx: w; kDw: x
