@@ -67,19 +67,18 @@ def check(kind, rows, groups, N, K):
         ref = torch.full(shape, FILL, dtype=torch.float64, device="cuda")
         if kind == "fp8":
             xs, ws = _pow2(g, rows, nb), _pow2(g, groups, -(-N // 128), nb)
-            xv = x.double() * _spread(xs, K, 1).double()
-        else:
-            xv = x.double()
         for i, (lo, hi) in enumerate(spans):
+            xi = x[lo:hi].double()
             if kind == "dw":
-                ref[i] = b[lo:hi].double().t() @ xv[lo:hi]
+                ref[i] = b[lo:hi].double().t() @ xi
                 continue
             if hi == lo:
                 continue
             wi = w[i].double()
             if kind == "fp8":
-                wi = wi * _spread(_spread(ws[i], N, 0), K, 1).double()
-            ref[lo:hi] = xv[lo:hi] @ (wi if kind == "dx" else wi.t())
+                xi *= _spread(xs[lo:hi], K, 1)
+                wi *= _spread(_spread(ws[i], N, 0), K, 1)
+            ref[lo:hi] = xi @ (wi if kind == "dx" else wi.t())
         for out in ("f32", "bf16" if t == "fp8" else t):
             d = mx.Linear(rows, N, K, groups=groups, in_type=t, out_type=out)
             y = torch.full(shape, FILL, dtype=T[out], device="cuda")
@@ -100,5 +99,14 @@ def check(kind, rows, groups, N, K):
 @pytest.mark.parametrize("kind,case", [(k, c) for k in lc.SHAPES for c in lc.SHAPES[k]],
                          ids=lambda v: v if isinstance(v, str) else "-".join(map(str, v)))
 def test_every_shape(kind, case):
+    print(f"[case] {kind} shape {case[0]}: rows={case[1]} groups={case[2]} N={case[3]} K={case[4]}", flush=True)
+    check(kind, *case[1:])
+
+
+@pytest.mark.parametrize("kind,case", [(k, c) for k in lc.STREAMED for c in lc.STREAMED[k]],
+                         ids=lambda v: v if isinstance(v, str) else "-".join(map(str, v)))
+def test_every_shape_with_weights_that_stream(kind, case):
+    """Over 100 MiB of weights: another instance of the main loop, with the
+    streaming cache policy on the weights' loads."""
     print(f"[case] {kind} shape {case[0]}: rows={case[1]} groups={case[2]} N={case[3]} K={case[4]}", flush=True)
     check(kind, *case[1:])

@@ -47,3 +47,17 @@ def test_shapes_are_the_ones_named(plan, kind):
     shapes = set(lc.RING) - ({6} if kind == "dw" else set())   # 192 rows cannot be read transposed
     assert {s for s, _ in seen} == shapes
     assert {split for _, split in seen} == {False, True}
+
+
+@pytest.mark.parametrize("kind", list(lc.STREAMED))
+def test_streamed_sizes_take_the_streaming_policy(plan, kind):
+    seen = set()
+    for shape, rows, groups, N, K in lc.STREAMED[kind]:
+        p = plan(kind, rows, groups, N, K)
+        assert p["shape"] == shape and p["streams"], (kind, rows, groups, N, K, p)
+        if shape >= 0:   # row tiles of the average group: within those for which weights are read once
+            assert p["stages"] >= lc.stages(kind, shape), (kind, rows, groups, N, K, p)
+            assert rows <= groups * p["tb"] * (8 if kind == "dx" else 1), (kind, rows, groups, N, K, p)
+        seen.add((shape, p["splits"] > 1))
+    assert {s for s, _ in seen} == set(lc.RING) | (set() if kind == "dx" else {-1})
+    assert {split for s, split in seen if s >= 0} == {False, True}
