@@ -589,119 +589,95 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
 #endif
 }
 
-// ---- few rows: y for at most 16 TJ rows of a group at a time.  The weights
-// are read once, straight into the MFMA's operand registers: a block takes
-// 16 TI columns, its eight waves every eighth 128-byte piece of the rows, each
-// a chunk of CH pieces ahead; the waves' sums are added in order through LDS.
-// One launch, no partial sums in memory, and columns / 16 TI blocks a group.
+// ---- few rows: y for at most 16 rows in all.  The weights are read once,
+// straight into the MFMA's operand registers: a block takes 16 columns of a
+// group, its eight waves every eighth 128-byte piece of the rows, each kChunk
+// pieces ahead; the waves' sums are added in order through LDS.  One launch, no
+// partial sums in memory, and columns / 16 blocks a group.
 constexpr int kFewWaves = 8;
+constexpr int kChunk = 4;
 
 // NT: the weights with the streaming policy (one row, 4096 x 7168 in fp8, cached:
 // 9.5 us with it, 8.3 without).
-template <int IN, int TI, int TJ, int CH, bool NT>
+template <int IN, bool NT>
 __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int out_type) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int ES = IN == kFP8 ? 1 : 2;
-  __shared__ __align__(16) float red[kFewWaves][TI * TJ][256];
+  __shared__ __align__(16) float red[kFewWaves][256];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int g = blockIdx.y, c0 = blockIdx.x * 16 * TI;
+  const int g = blockIdx.y, c0 = blockIdx.x * 16;
   int lo, hi;
-  group_rows(p.off, g, p.rows, lo, hi);
+  group_rows(p.off, g, p.rows, lo, hi);  // p.rows <= 16
+  if (hi == lo) return;
+  const int nr = hi - lo;
   const uint32_t rowb = (uint32_t)(p.K * ES);
   const int npc = (int)(rowb + 127) / 128;  // 128-byte pieces of a row
   const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
   const rsrc_t Ar = make_rsrc(static_cast<const uint8_t*>(p.a) + ((size_t)g * p.N + c0) * rowb,
-                              (uint32_t)min(16 * TI, p.N - c0) * rowb);
-  const float* wsp = IN == kFP8 ? p.as + ((size_t)g * nnb + c0 / 128) * nkb : nullptr;
-  for (int r0 = lo; r0 < hi; r0 += 16 * TJ) {
-    const int nr = min(16 * TJ, hi - r0);
-    const rsrc_t Br = make_rsrc(static_cast<const uint8_t*>(p.b) + (size_t)r0 * rowb, (uint32_t)nr * rowb);
-    const rsrc_t Sr = make_rsrc(IN == kFP8 ? p.bs + (size_t)r0 * nkb : nullptr, IN == kFP8 ? (uint32_t)(nr * nkb) * 4u : 0u);
-    const rsrc_t Tr = make_rsrc(wsp, IN == kFP8 ? (uint32_t)nkb * 4u : 0u);
-    v4f acc[TI][TJ];
+                              (uint32_t)min(16, p.N - c0) * rowb);
+  const rsrc_t Br = make_rsrc(static_cast<const uint8_t*>(p.b) + (size_t)lo * rowb, (uint32_t)nr * rowb);
+  const rsrc_t Sr = make_rsrc(IN == kFP8 ? p.bs + (size_t)lo * nkb : nullptr, IN == kFP8 ? (uint32_t)(nr * nkb) * 4u : 0u);
+  const rsrc_t Tr = make_rsrc(IN == kFP8 ? p.as + ((size_t)g * nnb + c0 / 128) * nkb : nullptr,
+                              IN == kFP8 ? (uint32_t)nkb * 4u : 0u);
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  struct Piece {
+    v4i a[2], b[2];
+    int xs, ws;
+  };
+  Piece buf[2][kChunk];
+  // piece pc of the row: lane (l16, q) takes bytes [16 q, 16 q + 16) and the
+  // same of its upper half; past the row's or the tensor's end, zeros
+  auto fetch = [&](Piece& x, int pc) {
+    const uint32_t o = (uint32_t)pc * 128u + 16u * q;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    struct Piece {
-      v4i a[TI][2], b[TJ][2];
-      int xs[TJ], ws;
-    };
-    Piece buf[2][CH];
-    // piece pc of the row: lane (l16, q) takes bytes [16 q, 16 q + 16) and the
-    // same of its upper half; past the row's or the tensor's end, zeros
-    auto fetch = [&](Piece& x, int pc) {
-      const uint32_t o = (uint32_t)pc * 128u + 16u * q;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = o + 64u * h < rowb;
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-          x.a[i][h] = buf_load16_p<NT ? 2 : 0>(Ar, in ? (uint32_t)(16 * i + l16) * rowb + o + 64u * h : kOob, 0);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          x.b[j][h] = buf_load16(Br, in ? (uint32_t)(16 * j + l16) * rowb + o + 64u * h : kOob, 0);
-      }
-      if constexpr (IN == kFP8) {
-        x.ws = buf_load4(Tr, pc < nkb ? 4u * pc : kOob, 0);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          x.xs[j] = buf_load4(Sr, pc < nkb ? (uint32_t)((16 * j + l16) * nkb + pc) * 4u : kOob, 0);
-      }
-    };
-    auto add = [&](const Piece& x) {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        if constexpr (IN == kFP8) {
-          const float s = __int_as_float(x.xs[j]) * __int_as_float(x.ws);
-#pragma unroll
-          for (int i = 0; i < TI; ++i) {
-            const v8i a = __builtin_shufflevector(x.a[i][0], x.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const v8i b = __builtin_shufflevector(x.b[j][0], x.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const v4f d = mfma8(a, b, v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < TI; ++i) acc[i][j] = mfma16<IN>(x.a[i][h], x.b[j][h], acc[i][j]);
-        }
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < CH; ++k) fetch(buf[0][k], wave + kFewWaves * k);
-    for (int p0 = wave; p0 < npc; p0 += 2 * CH * kFewWaves) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int base = p0 + h * CH * kFewWaves;
-#pragma unroll
-        for (int k = 0; k < CH; ++k) fetch(buf[h ^ 1][k], base + (CH + k) * kFewWaves);
-#pragma unroll
-        for (int k = 0; k < CH; ++k) add(buf[h][k]);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = o + 64u * h < rowb ? (uint32_t)l16 * rowb + o + 64u * h : kOob;
+      x.a[h] = buf_load16_p<NT ? 2 : 0>(Ar, at, 0);
+      x.b[h] = buf_load16(Br, at, 0);
     }
-    if (r0 > lo) __syncthreads();  // the sums of the rows before have been read
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(&red[wave][i * TJ + j][l16 * 16 + 4 * q]) = acc[i][j];
-    __syncthreads();
-    for (int t = tid; t < TI * TJ * 256; t += kFewWaves * 64) {
-      const int tile = t >> 8, r = (tile % TJ) * 16 + ((t >> 4) & 15), c = c0 + (tile / TJ) * 16 + (t & 15);
-      float s = red[0][tile][t & 255];
-#pragma unroll
-      for (int w = 1; w < kFewWaves; ++w) s += red[w][tile][t & 255];
-      if (r < nr && c < p.N) {
-        const size_t o = (size_t)(r0 + r) * p.N + c;
-        if (out_type == kF32) static_cast<float*>(p.out)[o] = s;
-        else if (out_type == kF16) static_cast<_Float16*>(p.out)[o] = (_Float16)s;
-        else static_cast<__bf16*>(p.out)[o] = (__bf16)s;
-      }
+    if constexpr (IN == kFP8) {
+      x.ws = buf_load4(Tr, pc < nkb ? 4u * pc : kOob, 0);
+      x.xs = buf_load4(Sr, pc < nkb ? (uint32_t)(l16 * nkb + pc) * 4u : kOob, 0);
     }
+  };
+  auto add = [&](const Piece& x) {
+    if constexpr (IN == kFP8) {
+      const float s = __int_as_float(x.xs) * __int_as_float(x.ws);
+      const v8i a = __builtin_shufflevector(x.a[0], x.a[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const v8i b = __builtin_shufflevector(x.b[0], x.b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const v4f d = mfma8(a, b, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e], s, acc[e]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc = mfma16<IN>(x.a[h], x.b[h], acc);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) fetch(buf[0][k], wave + kFewWaves * k);
+  for (int p0 = wave; p0 < npc; p0 += 2 * kChunk * kFewWaves) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int base = p0 + h * kChunk * kFewWaves;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) fetch(buf[h ^ 1][k], base + (kChunk + k) * kFewWaves);
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) add(buf[h][k]);
+    }
+  }
+  *reinterpret_cast<v4f*>(&red[wave][l16 * 16 + 4 * q]) = acc;
+  __syncthreads();
+  const int r = tid >> 4, c = c0 + (tid & 15);
+  if (r < nr && c < p.N) {
+    float s = red[0][tid];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += red[w][tid];
+    const size_t o = (size_t)(lo + r) * p.N + c;
+    if (out_type == kF32) static_cast<float*>(p.out)[o] = s;
+    else if (out_type == kF16) static_cast<_Float16*>(p.out)[o] = (_Float16)s;
+    else static_cast<__bf16*>(p.out)[o] = (__bf16)s;
   }
 #endif
 }
@@ -750,17 +726,20 @@ hipError_t run_shape(const LinearArgs& p, const Plan& pl, hipStream_t st) {
 
 template <int IN, int OP>
 hipError_t run_op(int out_type, LinearArgs p, void* ws, hipStream_t st) {
+  const bool big = streams(IN, p.rows, p.N, p.K, p.groups);
+  if constexpr (OP == kFwd) {
+    if (few_rows(p.rows, p.N, p.groups)) {
+      const dim3 grid((unsigned)ceil_div(p.N, 16), p.groups);
+      if (big) k_linear_few<IN, true><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
+      else k_linear_few<IN, false><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
+      return hipGetLastError();
+    }
+  }
   Choice c = choose(OP, IN, p.rows, p.N, p.K, p.groups);
   c.plan.out_type = out_type;
-  c.plan.big = streams(IN, p.rows, p.N, p.K, p.groups);
+  c.plan.big = big;
   p.part = ws;
   hipError_t e;
-  if (OP == kFwd && few_rows(p.rows, p.N, p.groups)) {
-    const dim3 grid((unsigned)ceil_div(p.N, 16), p.groups);
-    if (c.plan.big) k_linear_few<IN, 1, 1, 4, true><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
-    else k_linear_few<IN, 1, 1, 4, false><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
-    return hipGetLastError();
-  }
   if (c.shape == 0) e = run_shape<Shape<IN, OP, 256, 256, 2, 4, 1, 2, 1>>(p, c.plan, st);
   else if (c.shape == 1) e = run_shape<Shape<IN, OP, 256, 128, 4, 2, 1, 3, 1>>(p, c.plan, st);
   else if (c.shape == 2) e = run_shape<Shape<IN, OP, 128, 128, 2, 2, 1, 2, 2>>(p, c.plan, st);
