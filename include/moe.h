@@ -388,7 +388,8 @@ int moe_forward_noalloc(const moe_dims_t* dims, moe_path_t path, const uint16_t*
  * outside are clamped, so nothing outside the tensors is touched).  NULL is
  * allowed for groups == 1 and means all rows.  Groups may be empty.  Rows in
  * no group are not written by the row products.  moe_quant_permute's
- * `offsets` are such offsets.
+ * `offsets` are such offsets.  `rows` may be a capacity, as there, but how the
+ * work is divided is chosen for `rows` rows: the closer, the faster.
  * Sums and scales are f32; each output is rounded once, to nearest even.
  * Results do not depend on timing: there are no atomic sums.
  * Conventions as above (device pointers, 16-byte alignment, asynchronous on
@@ -436,7 +437,8 @@ int moe_fp8_swiglu_quant(int32_t rows, int32_t K, int32_t x_type, const void* x,
  * xq u8 [rows, K], xs f32 [rows, ceil(K/128)], w u8 [groups, N, K], ws f32
  * [groups, ceil(N/128), ceil(K/128)], y [rows, N] of out_type.  d->in_type FP8.
  * Inside a block the matrix instruction aligns 32 products to the largest of
- * them and keeps about 14 bits below its leading one; everything after is f32. */
+ * them and keeps about 14 bits below its leading one; everything after is f32,
+ * the product xs * ws first (below 2^-126 it loses bits). */
 int moe_fp8_linear(const moe_linear_t* d, const uint8_t* xq, const float* xs, const uint8_t* w, const float* ws,
                    const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 

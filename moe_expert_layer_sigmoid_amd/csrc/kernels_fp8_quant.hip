@@ -81,7 +81,7 @@ __device__ __forceinline__ float silu_mul_far(float g, float u) {
 }
 
 // One thread per 16 columns, 8 threads per block of 128: every load and store
-// is 16 bytes.  Bound by memory: 15.2 us at 8192 x 2048 behind SwiGLU (84 MB, 5.5
+// is 16 bytes.  Bound by memory: 14.9 us at 8192 x 2048 behind SwiGLU (84 MB, 5.6
 // TB/s; a copy reaches 5.0); 8-column threads with scalar loads took 34.3.
 template <int XT, bool SWIGLU>
 __global__ void __launch_bounds__(kQuantThreads)

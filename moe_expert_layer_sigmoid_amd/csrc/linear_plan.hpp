@@ -30,14 +30,18 @@ struct Plan {
 constexpr int kMaxSplits = 16;
 constexpr size_t kPartMax = (size_t)64 << 20;  // partial sums of a split reduction, at most
 constexpr int kCus = 256;
-constexpr size_t kStreamMin = (size_t)100 << 20;  // weights larger than this do not stay cached from call to call
+// Weights larger than this are taken not to stay in the 256 MB memory-side cache
+// until their next use.  (Measured with calls on the same weights one after the
+// other; a program that runs other layers in between finds smaller ones cold too.)
+constexpr size_t kStreamMin = (size_t)100 << 20;
 
 // Block shapes and their costs (us, but for the factor of a product's kind
 // below): a stage of a block that has its compute unit to itself on a half-empty
 // card (`alone`), a stage per compute unit with every one full (`full`), and a
 // block's start and end (`edge`).  These and the constants of choose() are
 // fitted to the times of every shape and split on 1040 products (260 random
-// sizes, 1 to 8192 rows, 1 to 48 groups, widths 64 to 8192).
+// sizes, 1 to 8192 rows, 1 to 48 groups, widths 64 to 8192); fp8's two factors
+// were set by hand (1.8 % from the best on average; the fit's, 1.24 and 1.39: 1.7).
 struct Cost {
   int ta, tb, occ;
   float alone, full, edge;
@@ -67,8 +71,12 @@ struct Choice {
 //   max(rounds of blocks in sequence, the work at the full card's rate, the
 //   staged bytes at 14.8 TB/s) + the join of the splits.
 // The groups' sizes are on the device; the estimate takes them as equal, with
-// half a tile of waste each.  (On these and 280 further products the
-// choice is 2.0 % from the best on average.)
+// half a tile of waste each, and all of `rows` as in use.  On 1256 products the
+// choice is 2.0 % from the best on average, 6.8 % at the 90th percentile, 29 % at
+// the 99th and 66 % at worst (dw of 1667 rows, 24 groups, 2024 x 256: 22 us for
+// 13): nothing here counts the bytes past L2.  Where `rows` is a capacity of
+// eight times the rows in groups, it is 31 % from the best on average (485 forward
+// and dx products by group), 86 % at the 90th percentile.
 inline Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
   const int re = in_type == kFP8 ? 128 : 64;
   const int cols = op == kFwd ? N : K;
@@ -121,7 +129,7 @@ inline Choice choose(int op, int in_type, int rows, int N, int K, int groups) {
 
 // The forward product of a few rows in all takes k_linear_few while the blocks
 // of groups with rows are no more than the compute units, and those of groups
-// without few enough to come and go (measured: one row, 4096 x 7168: 8.3 us
+// without few enough to come and go (measured: one row, 4096 x 7168: 7.9 us
 // against 10.4 by tiles; 9 rows of 11 groups, 1140 x 752, up to 648 live blocks:
 // 12.3 us against 7.6).
 inline bool few_rows(int rows, int N, int groups) {
