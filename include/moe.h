@@ -458,6 +458,102 @@ int moe_grouped_linear_dx(const moe_linear_t* d, const void* dy, const void* w, 
 int moe_grouped_linear_dw(const moe_linear_t* d, const void* dy, const void* x, const int32_t* offsets, void* dw,
                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * What a product by expert is followed by, and the gradient through it.  16-bit
+ * operands (in_type BF16 or F16); sizes, groups and conventions as above.
+ *   z = x w_g^T + b_g,   y = act(z) + residual                     (gated 0)
+ *                        y = act(z[:, :F]) * z[:, F:] + residual   (gated 1, N = 2 F)
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,     /* z / (1 + e^-z); gated: SwiGLU */
+  MOE_ACT_GELU = 3,     /* z Phi(z) */
+  MOE_ACT_GELU_TANH = 4 /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+} moe_act_t;
+
+/* Workspace bytes of the two calls below on these sizes (any activation).  May
+ * be 0; 0 for invalid sizes too.  No bound for fewer rows, which may need more. */
+size_t moe_linear_act_workspace_bytes(const moe_linear_t* d);
+
+/* The product with its epilogue.  x [rows, K], w [groups, N, K] and bias [groups,
+ * N] (nullable) of in_type; residual (nullable) and y [rows, N], gated [rows,
+ * N / 2], of out_type; pre (nullable) [rows, N] of out_type receives z, for the
+ * gradient.  N must be even if gated.  residual may be y itself.  The sum, bias,
+ * activation and residual are f32, y and z each rounded once (y is not made from
+ * the rounded z).  Rows in no group are not written, in y and in pre.  An
+ * infinite z gives what the formula gives: NaN where it has 0 * infinity. */
+int moe_grouped_linear_act(const moe_linear_t* d, int32_t act, int32_t gated, const void* x, const void* w,
+                           const void* bias, const void* residual, const int32_t* offsets, void* y, void* pre,
+                           void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* The gradient through bias and activation, for dy = dL/dy and z = pre:
+ *   dz = dy act'(z),  gated: (dy z[:, F:] act'(z[:, :F]), dy act(z[:, :F]));
+ *   db_g = sum over the group's rows of dz (zeros for an empty group).
+ * dy [rows, N], gated [rows, N / 2], and pre [rows, N] of out_type; dz [rows, N]
+ * of in_type, what moe_grouped_linear_dx and _dw take as dy; db (nullable) f32
+ * [groups, N], overwritten, added up from the f32 values before their rounding.
+ * (The residual's gradient is dy.)  relu'(0) = 0.  N a multiple of 8; K is not
+ * used but must be valid.  dz may be pre itself where the types are the same.
+ * The workspace is needed for db alone.  One launch, or two for db. */
+int moe_grouped_linear_act_backward(const moe_linear_t* d, int32_t act, int32_t gated, const void* dy, const void* pre,
+                                    const int32_t* offsets, void* dz, float* db, void* workspace,
+                                    size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The global gradient norm and clipping by it.  `tensors` is a HOST array that
+ * is read during the call alone; its pointers are device pointers, aligned to
+ * their element.  Captured into a graph, a call keeps the addresses that it was
+ * given.  The workspace (moe_grad_workspace_bytes(count), 16-byte aligned) is
+ * needed by every call.  Sums are f64 and added in a fixed order.
+ * ------------------------------------------------------------------------- */
+#define MOE_GRAD_MAX_TENSORS 65536
+typedef struct {
+  const void* in;
+  void* out;    /* moe_grad_clip writes here; may be its own `in`, else no outputs and inputs overlap.
+                   moe_grad_norm: not used */
+  int64_t n;    /* elements, 0 to 2^36 */
+  int32_t type; /* BF16, F16 or F32, of both */
+  int32_t reserved;
+} moe_tensor_t;
+
+size_t moe_grad_workspace_bytes(int32_t count);
+
+/* norm f32 [1] (device, 4-byte aligned) = sqrt(sum over all tensors of in^2).
+ * ceil(count / 112) + 1 launches. */
+int moe_grad_norm(const moe_tensor_t* tensors, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                  moe_stream_t stream);
+
+/* out = in * min(1, max_norm / (norm + 1e-6)), rounded once; norm (nullable)
+ * receives the norm before.  max_norm >= 0.  A NaN among the values makes every
+ * output NaN; an infinity makes the factor 0 (and itself NaN).  2 ceil(count / 112)
+ * launches. */
+int moe_grad_clip(const moe_tensor_t* tensors, int32_t count, float max_norm, float* norm, void* workspace,
+                  size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The whole layer, a1..a7, on unquantised experts for a few tokens: a16w16.
+ * Routing, remap and record as moe_forward; then for each local pair (t, j),
+ * e its slot,  h = w1_e x_t,  act = silu(h[:F]) * h[F:],  out_t = sum over j of
+ * topk_w[t][j] w2_e act.  x and out [T, H], w1 [P_local, 2F, H] and w2 [P_local,
+ * H, F] of `type` (BF16 or F16), in their natural layout, as moe_grouped_linear
+ * takes them.  Sums, activation and weights are f32; topk_w * act is rounded to
+ * `type` before the second product (F16: finite up to 65504) and out at the end.
+ * Tokens with no local pair get +0.  T <= 32, else MOE_ERR_UNSUPPORTED (more
+ * tokens: moe_quant_permute's buckets with moe_grouped_linear_act).
+ * num_tokens (nullable, DEVICE i32, 4-byte aligned): the step's token count n,
+ * read by the kernels and clamped to [0, T], for captured graphs as in
+ * moe_forward_small_m: rows [n, T) of out are +0, load_hist counts the first n.
+ * taps (nullable): topk_ids, topk_w and phys_ids are written for the first n
+ * tokens (phys_ids of the others: -1), other members ignored.  Workspace:
+ * moe_a16w16_workspace_bytes(dims), 256-byte aligned.  Two launches.
+ * ------------------------------------------------------------------------- */
+size_t moe_a16w16_workspace_bytes(const moe_dims_t* dims);
+int moe_forward_a16w16(const moe_dims_t* dims, int32_t type, const int32_t* num_tokens, const void* x,
+                       const float* logits, const void* w1, const void* w2, const int32_t* rep_count,
+                       const int32_t* rep_slots, int32_t* load_hist, void* out, const moe_taps_t* taps, void* workspace,
+                       size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,7 +35,10 @@ EXPORTS = ("moe_workspace_bytes", "moe_select_path", "moe_status_string", "moe_p
            "moe_router_workspace_bytes", "moe_router_logits", "moe_forward_small_m",
            "moe_a16w4_workspace_bytes", "moe_forward_a16w4", "moe_forward_noalloc", "moe_replica_of",
            "moe_linear_workspace_bytes", "moe_fp8_quant", "moe_fp8_swiglu_quant", "moe_fp8_linear",
-           "moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw")
+           "moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw",
+           "moe_linear_act_workspace_bytes", "moe_grouped_linear_act", "moe_grouped_linear_act_backward",
+           "moe_grad_workspace_bytes", "moe_grad_norm", "moe_grad_clip",
+           "moe_a16w16_workspace_bytes", "moe_forward_a16w16")
 
 
 class MoeError(RuntimeError):
@@ -62,6 +65,7 @@ class Dims(ctypes.Structure):
 
 TYPES = {"bf16": 0, "f16": 1, "f32": 2, "fp8": 3}   # moe_type_t
 _TORCH_TYPES = (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn)
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # moe_act_t
 _QUANT_TYPES = {t: i for i, t in enumerate(_TORCH_TYPES[:3])}
 
 
@@ -161,6 +165,21 @@ def lib() -> ctypes.CDLL:
         L.moe_fp8_linear.restype = I
         for n in ("moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw"):
             getattr(L, n).argtypes = [N, P, P, P, P, P, S, P]
+            getattr(L, n).restype = I
+        C = ctypes.c_int32
+        L.moe_linear_act_workspace_bytes.argtypes = [N]
+        L.moe_linear_act_workspace_bytes.restype = S
+        L.moe_grouped_linear_act.argtypes = [N, C, C, P, P, P, P, P, P, P, P, S, P]
+        L.moe_grouped_linear_act_backward.argtypes = [N, C, C, P, P, P, P, P, P, S, P]
+        L.moe_grad_workspace_bytes.argtypes = [C]
+        L.moe_grad_workspace_bytes.restype = S
+        L.moe_grad_norm.argtypes = [P, C, P, P, S, P]
+        L.moe_grad_clip.argtypes = [P, C, ctypes.c_float, P, P, S, P]
+        L.moe_a16w16_workspace_bytes.argtypes = [D]
+        L.moe_a16w16_workspace_bytes.restype = S
+        L.moe_forward_a16w16.argtypes = [D, C, P, P, P, P, P, P, P, P, P, ctypes.POINTER(Taps), P, S, P]
+        for n in ("moe_grouped_linear_act", "moe_grouped_linear_act_backward", "moe_grad_norm", "moe_grad_clip",
+                  "moe_forward_a16w16"):
             getattr(L, n).restype = I
         for n in ("moe_pack_weights", "moe_route", "moe_eplb_remap_record", "moe_quant_permute",
                   "moe_grouped_gemm1_swiglu", "moe_grouped_gemm2_combine", "moe_grouped_gemm1_swiglu_pairs",
@@ -721,3 +740,173 @@ def moe_grouped_linear_dw(d: Linear, dy, x, dw, scratch, offsets=None, stream=No
                  stream)
     elif rc:
         raise MoeError("moe_grouped_linear_dw", rc)
+
+
+# ----------------------------------------------------------------------------
+# Products with an epilogue, the gradient through it, clipping
+# ----------------------------------------------------------------------------
+
+def moe_linear_act_workspace_bytes(d: Linear) -> int:
+    return int(lib().moe_linear_act_workspace_bytes(ctypes.byref(d)))
+
+
+def linear_act_workspace(d: Linear, device="cuda") -> torch.Tensor:
+    """A workspace for moe_grouped_linear_act and its backward on ``d``'s sizes."""
+    return torch.empty(max(moe_linear_act_workspace_bytes(d), 256), dtype=u8, device=device)
+
+
+def _act(act: str) -> int:
+    a = ACTS.get(act)
+    if a is None:
+        raise ValueError(f"act: {act!r} is none of {', '.join(ACTS)}")
+    return a
+
+
+def _opt(t, name, dtype, numel_min, dev):
+    return None if t is None else _addr(t, name, dtype, numel_min, dev)
+
+
+def moe_grouped_linear_act(d: Linear, x, w, y, scratch, act: str = "none", gated: bool = False, bias=None,
+                           residual=None, pre=None, offsets=None, stream=None) -> None:
+    """y = act(z) + residual with z = x [rows, K] times each group's w [N, K]
+    transposed, plus its bias [N] (bias: [groups, N]); ``gated``: y [rows, N/2]
+    = act(z[:, :N/2]) * z[:, N/2:] + residual.  ``act``: "none", "relu", "silu",
+    "gelu", "gelu_tanh".  x, w and bias of d's in_type, y, residual and pre of
+    its out_type.  ``residual`` may be y; ``pre`` [rows, N] receives z."""
+    a = _act(act)
+    dev = _device(y, "y")
+    t, o = _TORCH_TYPES[d.in_type], _TORCH_TYPES[d.out_type]
+    n = d.rows * (d.N // 2 if gated else d.N)
+    _launch("moe_grouped_linear_act", dev, stream, ctypes.byref(d), a, int(bool(gated)),
+            _addr(x, "x", t, d.rows * d.K, dev), _addr(w, "w", t, d.groups * d.N * d.K, dev),
+            _opt(bias, "bias", t, d.groups * d.N, dev), _opt(residual, "residual", o, n, dev), _offsets(d, offsets, dev),
+            _addr(y, "y", o, n, dev), _opt(pre, "pre", o, d.rows * d.N, dev), *_scratch(scratch, dev))
+
+
+def moe_grouped_linear_act_backward(d: Linear, dy, pre, dz, scratch, act: str = "none", gated: bool = False, db=None,
+                                    offsets=None, stream=None) -> None:
+    """dz [rows, N] (d's in_type) of dy [rows, N] (gated: N/2) and pre [rows, N]
+    (its out_type), through the activation; ``db`` float32 [groups, N] receives
+    the bias's gradient (zeros for an empty group)."""
+    a = _act(act)
+    dev = _device(dz, "dz")
+    o = _TORCH_TYPES[d.out_type]
+    _launch("moe_grouped_linear_act_backward", dev, stream, ctypes.byref(d), a, int(bool(gated)),
+            _addr(dy, "dy", o, d.rows * (d.N // 2 if gated else d.N), dev), _addr(pre, "pre", o, d.rows * d.N, dev),
+            _offsets(d, offsets, dev), _addr(dz, "dz", _TORCH_TYPES[d.in_type], d.rows * d.N, dev),
+            _opt(db, "db", f32, d.groups * d.N, dev), *_scratch(scratch, dev))
+
+
+class _Tensor(ctypes.Structure):
+    """moe_tensor_t"""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class GradList:
+    """Tensors (bfloat16, float16 or float32, contiguous, on one device) for
+    moe_grad_norm and moe_grad_clip, and where the clipped ones go: ``outs`` of
+    the same sizes and types, or None for in place.  It holds the tensors, so
+    that their addresses stay theirs; make a new one when gradients move."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"outs: {len(self.outs)} tensors for {len(self.grads)}")
+        self.device = -1
+        self._array = (_Tensor * max(len(self.grads), 1))()
+        spans = []
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            name = f"grads[{i}]"
+            if i == 0:
+                self.device = _device(g, name)
+            t = _QUANT_TYPES.get(g.dtype) if isinstance(g, torch.Tensor) else None
+            if isinstance(g, torch.Tensor) and t is None:
+                raise TypeError(f"{name}: dtype {g.dtype}, expected bfloat16, float16 or float32")
+            a = _addr(g, name, getattr(g, "dtype", None), 0, self.device)
+            b = a if o is g else _addr(o, f"outs[{i}]", g.dtype, 0, self.device)
+            n = g.numel()
+            if o.numel() != n:
+                raise ValueError(f"outs[{i}]: {o.numel()} elements, expected {n}")
+            self._array[i] = _Tensor(a, b, n, t, 0)
+            if n:
+                size = n * g.element_size()
+                spans.append((b, b + size, i, True))
+                if a != b:
+                    spans.append((a, a + size, i, False))
+        # an output is written by one entry and read by none but its own
+        spans.sort()
+        end, by, out = -1, -1, False
+        for lo, hi, i, is_out in spans:
+            if lo < end and (is_out or out):
+                raise ValueError(f"tensors {by} and {i} overlap")
+            if hi > end:
+                end, by, out = hi, i, is_out
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def moe_grad_workspace_bytes(count: int) -> int:
+    return int(lib().moe_grad_workspace_bytes(int(count)))
+
+
+def grad_workspace(grads: GradList, device=None) -> torch.Tensor:
+    """A workspace for moe_grad_norm and moe_grad_clip on this list."""
+    device = torch.device("cuda", grads.device) if device is None and grads.device >= 0 else device or "cuda"
+    return torch.empty(max(moe_grad_workspace_bytes(len(grads)), 256), dtype=u8, device=device)
+
+
+def _grad(fn: str, grads: GradList, norm, scratch, stream, *args) -> None:
+    if not isinstance(grads, GradList):
+        raise TypeError("grads: expected a GradList")
+    dev = grads.device if len(grads) else _device(scratch, "workspace")
+    _launch(fn, dev, stream, ctypes.addressof(grads._array), len(grads), *args, _opt(norm, "norm", f32, 1, dev),
+            *_scratch(scratch, dev))
+
+
+def moe_grad_norm(grads: GradList, norm, scratch, stream=None) -> None:
+    """norm float32 [1] = sqrt(sum of squares over all of the list's tensors)."""
+    _grad("moe_grad_norm", grads, norm, scratch, stream)
+
+
+def moe_grad_clip(grads: GradList, max_norm: float, norm, scratch, stream=None) -> None:
+    """The list's outs = its grads times min(1, max_norm / (norm + 1e-6)); ``norm``
+    (float32 [1] or None) receives the norm before."""
+    _grad("moe_grad_clip", grads, norm, scratch, stream, float(max_norm))
+
+
+# ----------------------------------------------------------------------------
+# a16w16: the layer on unquantised experts for a few tokens
+# ----------------------------------------------------------------------------
+
+def moe_a16w16_workspace_bytes(d: Dims) -> int:
+    return int(lib().moe_a16w16_workspace_bytes(ctypes.byref(d)))
+
+
+def a16w16_workspace(d: Dims, device="cuda") -> torch.Tensor:
+    return torch.empty(max(moe_a16w16_workspace_bytes(d), 256), dtype=u8, device=device)
+
+
+def moe_forward_a16w16(d: Dims, x, logits, w1, w2, rep_count, rep_slots, out, ws, num_tokens=None, load_hist=None,
+                       taps: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> None:
+    """The layer on bfloat16 or float16 experts w1 [P_local, 2F, H] and w2
+    [P_local, H, F] for at most 32 tokens; x and out [T, H] of their type.
+    ``num_tokens`` (int32 device tensor, one element): the step's token count,
+    read by the kernels, for captured graphs.  ``taps``: topk_ids, topk_w,
+    phys_ids."""
+    dev = _device(out, "out")
+    if not isinstance(x, torch.Tensor) or x.dtype not in _TORCH_TYPES[:2]:
+        raise TypeError("x: expected a bfloat16 or float16 torch.Tensor")
+    TK, _ = _sizes(d)
+    t = x.dtype
+    tp = None
+    if taps is not None:
+        tp = Taps(**{n: _opt(taps.get(n), n, dt, TK, dev) for n, dt in (("topk_ids", i32), ("topk_w", f32), ("phys_ids", i32))})
+    _launch("moe_forward_a16w16", dev, stream, ctypes.byref(d), _QUANT_TYPES[t], _opt(num_tokens, "num_tokens", i32, 1, dev),
+            _addr(x, "x", t, d.T * d.H, dev), _addr(logits, "logits", f32, d.T * d.E, dev),
+            _addr(w1, "w1", t, d.P_local * 2 * d.F * d.H, dev), _addr(w2, "w2", t, d.P_local * d.H * d.F, dev),
+            _addr(rep_count, "rep_count", i32, d.E, dev), _addr(rep_slots, "rep_slots", i32, d.E * d.R_max, dev),
+            _opt(load_hist, "load_hist", i32, d.P_total, dev), _addr(out, "out", t, d.T * d.H, dev),
+            ctypes.byref(tp) if tp is not None else None, *_scratch(ws, dev))

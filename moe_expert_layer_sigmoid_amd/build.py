@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 BIND = os.path.join(PKG, "_bind.so")
 SOURCES = ["moe_api.hip", "kernels_front.hip", "kernels_gemm.hip", "kernels_tiled.hip", "eplb.hip",
            "kernels_router.hip", "kernels_a16.hip", "linear_api.hip", "kernels_linear.hip",
-           "kernels_fp8_quant.hip"]
+           "kernels_fp8_quant.hip", "kernels_linear_act.hip", "kernels_linear_act_f16.hip",
+           "kernels_act_backward.hip", "kernels_grad.hip", "kernels_a16w16.hip"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 
@@ -67,9 +68,9 @@ def _build_bind(verbose: bool) -> None:
 
 def build(verbose: bool = False) -> str:
     objs = [os.path.join(CSRC, src.replace(".hip", ".o")) for src in SOURCES]
+    jobs = sorted(zip(SOURCES, objs), key=lambda so: "linear" not in so[0])   # the longest first
     with ThreadPoolExecutor(4) as ex:
-        list(ex.map(lambda so: _run([hipcc(), *flags(), "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose, so[0]),
-                    zip(SOURCES, objs)))
+        list(ex.map(lambda so: _run([hipcc(), *flags(), "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose, so[0]), jobs))
     tmp = LIB + ".tmp"
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmoe.so", "-o", tmp, *objs], verbose, "link")
     os.replace(tmp, LIB)

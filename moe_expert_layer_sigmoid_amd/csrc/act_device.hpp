@@ -1,0 +1,109 @@
+// Activations and their derivatives in f32, shared by the quantiser behind
+// SwiGLU, the products' epilogues and the gradient through them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+namespace moe {
+
+// e^-g from the hardware's exp2 (1 ulp), its argument carried in two parts:
+// one f32 product -g log2(e) would lose log2|g| bits of the result.
+__device__ __forceinline__ float exp_neg(float g) {
+  const float hi = g * -1.44269504f;
+  const float lo = fmaf(g, -1.44269504f, -hi) + g * -1.92596299e-8f;  // log2(e) = 1.44269504 + 1.92596299e-8
+  return __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.69314718f, 1.0f);
+}
+
+// silu(g) u for g >= kFarGate: the hardware's reciprocal (1 ulp) in place of a
+// division keeps the kernel on the memory's side of its balance (in all within
+// 9 x 2^-24 of the value, far below the codes' 2^-4).  Above 88 the sigmoid
+// rounds to 1, and e^-inf by the two parts above would be NaN.
+constexpr float kFarGate = -80.0f;
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float e = exp_neg(g);
+  const float r = g > 88.0f ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e);
+  return g * r * u;
+}
+
+// silu(g) u for g < kFarGate, where 1 + e^-g rounds to e^-g: g e^g u.  Below
+// -87 neither e^g nor its reciprocal is a normal f32, while the product may be
+// one (silu(-88) = -5e-37, times u): t = e^(g/4) is normal down to -349, where
+// no u brings the product back into range, and every partial product is
+// normal wherever the result is (four errors of t and five roundings: 21 x
+// 2^-24).  g = -inf: NaN, as in the formula.
+__device__ __forceinline__ float silu_mul_far(float g, float u) {
+  const float t = exp_neg(-0.25f * g);
+  return (g * t) * (u * t) * t * t;
+}
+
+// moe_act_t of include/moe.h
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActs = 5 };
+
+// g sigmoid(t) u.  t below kFarGate: e^t in four factors, as in silu_mul_far; below
+// -400 every factor is zero.  (Comparisons are written so that a NaN passes.)
+__device__ __forceinline__ float sigmoid_mul(float t, float g, float u) {
+  if (t < kFarGate) {
+    const float s = exp_neg(t < -400.0f ? 100.0f : -0.25f * t);
+    return (g * s) * (u * s) * s * s;
+  }
+  return g * (t > 88.0f ? 1.0f : __builtin_amdgcn_rcpf(1.0f + exp_neg(t))) * u;
+}
+
+constexpr float kGeluC = 0.797884561f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// act(g) u.  gelu: z Phi(z), by erfc so that the negative tail keeps its
+// relative error; gelu_tanh: 0.5 z (1 + tanh w) = z sigmoid(2 w) with
+// w = sqrt(2 / pi) (z + 0.044715 z^3).  The exponent's own rounding grows with it:
+// relative errors of up to (8 + z^2) 2^-23 (gelu) and (8 + |2 w|) 2^-22 (gelu_tanh).
+template <int ACT>
+__device__ __forceinline__ float act_mul(float g, float u) {
+  if constexpr (ACT == kActRelu) return (g < 0.0f ? 0.0f : g) * u;
+  else if constexpr (ACT == kActSilu) return g < kFarGate ? silu_mul_far(g, u) : silu_mul(g, u);
+  else if constexpr (ACT == kActGelu) return 0.5f * erfcf(g * -0.707106781f) * g * u;
+  else if constexpr (ACT == kActGeluTanh) return sigmoid_mul(2.0f * kGeluC * g * fmaf(kGeluA * g, g, 1.0f), g, u);
+  else return g * u;
+}
+
+// act'(z) v.
+//  silu:      s (1 + z (1 - s)), s = sigmoid(z); far below 0, e^z (1 + z)
+//  gelu:      Phi(z) + z phi(z)
+//  gelu_tanh: s + z s (1 - s) 2 w'(z), s = sigmoid(2 w), w' = sqrt(2 / pi) (1 + 3 0.044715 z^2);
+//             beyond 16 it is 1 or 0 in f32, and z^2 would overflow
+template <int ACT>
+__device__ __forceinline__ float slope_mul(float z, float v) {
+  if constexpr (ACT == kActRelu) {
+    return z <= 0.0f ? 0.0f : v;
+  } else if constexpr (ACT == kActSilu) {
+    if (z < kFarGate) {
+      const float t = exp_neg(z < -400.0f ? 100.0f : -0.25f * z);
+      return ((1.0f + z) * t) * (v * t) * t * t;
+    }
+    const float e = z > 88.0f ? 0.0f : exp_neg(z), s = __builtin_amdgcn_rcpf(1.0f + e);
+    return s * fmaf(z, e * s, 1.0f) * v;  // 1 - s = e s
+  } else if constexpr (ACT == kActGelu) {
+    const float h = 0.5f * z * z;
+    return fmaf(z, 0.398942280f * exp_neg(h > 200.0f ? 200.0f : h), 0.5f * erfcf(z * -0.707106781f)) * v;
+  } else if constexpr (ACT == kActGeluTanh) {
+    const float x = z > 16.0f ? 16.0f : z < -16.0f ? -16.0f : z;
+    const float x2 = x * x, t = 2.0f * kGeluC * x * fmaf(kGeluA, x2, 1.0f);
+    const float e = t > 88.0f ? 0.0f : exp_neg(t < -80.0f ? -80.0f : t), s = __builtin_amdgcn_rcpf(1.0f + e);
+    return s * fmaf(x * (e * s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f) * v;
+  } else {
+    return v;
+  }
+}
+
+// f(std::integral_constant<int, act>) for a runtime act.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
+  else if (act == kActRelu) f(std::integral_constant<int, kActRelu>{});
+  else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});
+  else if (act == kActGeluTanh) f(std::integral_constant<int, kActGeluTanh>{});
+  else f(std::integral_constant<int, kActNone>{});
+}
+
+}  // namespace moe

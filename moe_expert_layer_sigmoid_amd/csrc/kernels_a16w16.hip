@@ -1,0 +1,443 @@
+// The whole expert layer for a few tokens on 16-bit experts, in two launches:
+//   k_few_up    routing and remap of every token in every block (a token's logits
+//               are 1.5 KB in L2, a launch more costs longer); then, for 16
+//               columns of F of a touched slot, h = W1 x and
+//               act = round(w_tj silu(gate) up), the token's routing weight w_tj
+//               folded in before the one rounding to the operands' type (as the
+//               layer's other 16-bit variant rounds act; the sum over a token's
+//               experts then needs no second pass);
+//   k_few_down  out[t] = sum over the touched slots of W2 act: a block owns up to
+//               16 rows of H for all tokens and all slots, so that sums stay in
+//               f32 accumulators from the first slot to the last and nothing is
+//               joined in memory.
+// MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
+// experts' weights, read once; whole 128-byte lines go by DMA into an LDS ring that
+// belongs to one wave alone, with every 4th stage of the reduction its own, so that no wave waits
+// for another but at the end of a block's columns, and the next columns' weights
+// are then already on their way.  x and act rows (a few KB, from L2) are loaded
+// straight into the operand registers as far ahead.
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "act_device.hpp"
+#include "linear_kernel.hpp"
+#include "moe_internal.hpp"
+#include "route_device.hpp"
+
+namespace moe {
+
+constexpr int kPairs = kFewMaxT * 16;  // T k at most
+
+// The touched slots, ascending; their pairs are rows [start, start + popc(mask)),
+// one per bit (token) of mask, ascending.
+struct FewTable {
+  int n;
+  int pad[3];
+  uint32_t mask[kPairs];
+  uint16_t slot[kPairs], start[kPairs];
+};
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * 64;
+constexpr int kRingBytes = 16384;      // of a wave
+constexpr int kStageK = 64;            // reduction elements of a stage: 128 bytes of a row
+
+// A wave's ring: NA tiles of 16 weight rows a stage, NS stages, and the token
+// operands of those stages in registers.
+template <int TY, int NA, int NT>
+struct Ring {
+  static constexpr int kSlot = NA * 2048;
+  static constexpr int NS = kRingBytes / kSlot, PRE = NS - 1;
+  static constexpr int I = 2 * NA + 2 * NT;  // loads of a stage
+  static_assert((PRE - 1) * I < 63, "vmcnt range");
+  v4i b[NS][NT][2];
+  v4f acc[NA][NT];
+};
+
+template <int TY>
+using Half = std::conditional_t<TY == kBF16, __bf16, _Float16>;
+
+// ---- routing: the block's view of all tokens -------------------------------
+struct Routed {
+  FewTable tab;
+  uint8_t tok[kPairs];  // of a row: its token
+  float w[kPairs];      // ... and its routing weight
+};
+struct RouteScratch {
+  int phys[kPairs];
+  float w[kPairs];
+  uint32_t mask[1024];  // of a local slot: its tokens
+  int before[1024];     // ... and its index among the touched ones
+  int rep_slots[1024];
+};
+
+template <int EPL>
+__device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScratch& s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = p.t_dev ? min(max(*p.t_dev, 0), p.T) : p.T;
+  const bool flat = p.R_max == 1;  // one replica each: the slots are read beside the logits
+  for (int i = tid; i < p.P_local; i += kThreads) s.mask[i] = 0;
+  if (flat)
+    for (int i = tid; i < p.E; i += kThreads) s.rep_slots[i] = p.rep_slots[i];
+  __syncthreads();
+  const bool first = blockIdx.x == 0;
+  auto keep = [&](int t, int j, int e, float w) {
+    int ph;
+    e = min(e, p.E - 1);  // (NaN logits, against the contract, may choose past E)
+    if (flat) ph = s.rep_slots[e];
+    else ph = p.rep_slots[(size_t)e * p.R_max + replica(fmix32(p.base + (uint32_t)t), p.rep_count[e], p.R_max)];
+    s.phys[t * p.k + j] = ph;
+    s.w[t * p.k + j] = w;
+    const int q = ph - p.p0;
+    if (q >= 0 && q < p.P_local) atomicOr(&s.mask[q], 1u << t);
+    if (first) {
+      if (p.ids) p.ids[t * p.k + j] = e;
+      if (p.wts) p.wts[t * p.k + j] = w;
+      if (p.phys) p.phys[t * p.k + j] = ph;
+      if (p.load_hist && ph >= 0 && ph < p.P_total) atomicAdd(&p.load_hist[ph], 1);  // whole numbers: any order
+    }
+  };
+  if (n <= kWaves) {
+    if (wave < n) {
+      int e;
+      float w;
+      route64<EPL>(p.logits + (size_t)wave * p.E, p.E, p.k, lane, e, w);
+      if (lane < p.k) keep(wave, lane, e, w);
+    }
+  } else {
+    for (int t0 = 0; t0 < n; t0 += kThreads / 16) {
+      const int t = t0 + tid / 16;
+      int e;
+      float w;
+      route16<4 * EPL>(p.logits + (size_t)min(t, n - 1) * p.E, p.E, p.k, tid & 15, e, w);
+      if (t < n && (tid & 15) < p.k) keep(t, tid & 15, e, w);
+    }
+  }
+  if (first && p.phys)
+    for (int i = n * p.k + tid; i < p.T * p.k; i += kThreads) p.phys[i] = -1;
+  __syncthreads();
+  if (wave == 0) {  // the touched slots and their rows, 64 slots at a time
+    int nt = 0, rows = 0;
+    for (int c = 0; c < p.P_local; c += 64) {
+      const uint32_t m = c + lane < p.P_local ? s.mask[c + lane] : 0;
+      const unsigned long long any = __ballot(m != 0);
+      int pre = __popc(m);
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(pre, d);
+        if (lane >= d) pre += up;
+      }
+      if (m) {
+        const int i = nt + __popcll(any & ((1ull << lane) - 1));
+        s.before[c + lane] = i;
+        r.tab.slot[i] = (uint16_t)(c + lane);
+        r.tab.start[i] = (uint16_t)(rows + pre - __popc(m));
+        r.tab.mask[i] = m;
+      }
+      nt += __popcll(any);
+      rows += __builtin_amdgcn_readlane(pre, 63);
+    }
+    if (lane == 0) r.tab.n = nt;
+  }
+  __syncthreads();
+  // a row's token and weight (the sum, should two of a token's experts share a slot)
+  for (int i = tid; i < n * p.k; i += kThreads) {
+    const int t = i / p.k, q = s.phys[i] - p.p0;
+    if (q < 0 || q >= p.P_local) continue;
+    const int b = s.before[q], row = r.tab.start[b] + __popc(s.mask[q] & ((1u << t) - 1));
+    float w = 0.0f;
+    for (int j = 0; j < p.k; ++j)
+      if (s.phys[t * p.k + j] == s.phys[i]) w += s.w[t * p.k + j];
+    r.tok[row] = (uint8_t)t;
+    r.w[row] = w;
+  }
+  __syncthreads();
+}
+
+// ---- one stage --------------------------------------------------------------
+// Lane offsets of the DMA: 8 rows of 128 bytes an instruction, the 16-byte pieces
+// of a row permuted so that the reads spread over the LDS banks.
+__device__ __forceinline__ uint32_t dma_piece(int lane) { return 16u * (uint32_t)((lane & 7) ^ (lane >> 3)); }
+
+template <int TY, int NA, int NT>
+__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT>& g, int u) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const v4i w = *reinterpret_cast<const lds_v4i*>(rd + a * 2048 + l16 * 128 + (((4 * kk + q) ^ (l16 & 7)) * 16));
+#pragma unroll
+      for (int c = 0; c < NT; ++c) g.acc[a][c] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c]);
+    }
+}
+
+// The waves' sums of acc[a][c], by thread (token column tid / 16, weight row tid % 16).
+template <int NA>
+__device__ __forceinline__ void reduce(float (*red)[NA][256], const v4f (&v)[NA], float (&s)[NA]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) *reinterpret_cast<v4f*>(&red[wave][a][(lane & 15) * 16 + 4 * (lane >> 4)]) = v[a];
+  // (LDS alone is waited for: the loads of the next stages stay in flight)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    s[a] = red[0][a][tid];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s[a] += red[w][a][tid];
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int TY, int NT, int EPL>
+__global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using R = Ring<TY, 2, NT>;
+  __shared__ __align__(1024) uint8_t ring[kWaves * kRingBytes];
+  __shared__ __align__(16) float red[kWaves][2][256];
+  __shared__ Routed r;
+  static_assert(sizeof(RouteScratch) <= sizeof(ring), "scratch in the ring");
+  route_all<EPL>(p, r, *reinterpret_cast<RouteScratch*>(ring));
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
+  if (blockIdx.x == 0) {
+    const int m = r.tab.n;
+    if (tid == 0) p.tab->n = m;
+    for (int i = tid; i < m; i += kThreads) {
+      p.tab->slot[i] = r.tab.slot[i];
+      p.tab->start[i] = r.tab.start[i];
+      p.tab->mask[i] = r.tab.mask[i];
+    }
+  }
+  const int H = p.H, F = p.F, nct = F / 16;
+  const int items = __builtin_amdgcn_readfirstlane(r.tab.n) * nct;
+  const int kst = H / kStageK;
+  const int rounds = (kst + kWaves * R::NS - 1) / (kWaves * R::NS);
+  const uint32_t rowb = 2u * (uint32_t)H;
+  const uint32_t avo = (uint32_t)(lane >> 3) * rowb + dma_piece(lane);
+  const rsrc_t xr = make_rsrc(p.x, (uint32_t)p.T * rowb), none = make_rsrc(p.x, 0);
+
+  // where the next loads come from
+  int item = blockIdx.x, round = 0;
+  rsrc_t wr = none;
+  uint32_t wso = 0, xvo[NT];
+  auto seek = [&]() {  // of `item`
+    const bool live = item < items;
+    const int i = live ? item / nct : 0, ct = live ? item - i * nct : 0;
+    const int slot = __builtin_amdgcn_readfirstlane((int)r.tab.slot[i]);
+    const int start = r.tab.start[i], n = live ? __popc(r.tab.mask[i]) : 0;
+    wr = make_rsrc(static_cast<const uint8_t*>(p.w1) + (live ? (size_t)slot * 2 * F * rowb : 0), live ? 2u * (uint32_t)F * rowb : 0u);
+    wso = (uint32_t)ct * 16u * rowb;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const int j = 16 * c + l16;
+      xvo[c] = j < n ? (uint32_t)r.tok[start + j] * rowb + 16u * q : kOob;
+    }
+  };
+  R g;
+  auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
+    const int st = wave + kWaves * (R::NS * round + u);
+    const bool live = st < kst;
+    const uint32_t so = (uint32_t)st * 128u;
+    const rsrc_t a = live ? wr : none, x = live ? xr : none;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo,
+                                               so + wso + ((m & 1) * 8u + (m >> 1) * (uint32_t)F) * rowb, 0, 2);
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) g.b[u][c][kk] = buf_load16(x, xvo[c], so + 64u * kk);
+  };
+  // NS stages; before the first, the loads alone.  to and from are the same ring,
+  // as __restrict__: the compiler then places no wait of its own between a DMA in
+  // flight and the reads of another stage.
+  auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
+    if (first) {
+#pragma unroll
+      for (int u = 0; u < R::PRE; ++u) issue(to, u);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < R::NS; ++u) {
+      // stage u has landed; the reads of the stage before are done, whose slot is loaded next
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((R::PRE - 1) * R::I) : "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (u == 1) {  // the loads enter the next round
+        if (++round == rounds) {
+          round = 0;
+          item += gridDim.x;
+          seek();
+        }
+      }
+      issue(to, (u + R::PRE) % R::NS);
+      consume<TY, 2, NT>(from + u * R::kSlot, g, u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
+  if ((int)blockIdx.x >= items) return;  // fewer slots touched than pairs: the same in the whole block
+  seek();
+  int it = blockIdx.x;  // the item being added up
+  for (int n = -1;; ++n) {
+    if (n <= 0) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) g.acc[a][c] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    stages(mine, mine, n < 0);
+    if (n + 1 < rounds) continue;
+    const int i = it / nct, ct = it - i * nct;
+    const int start = r.tab.start[i], np = __popc(r.tab.mask[i]);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      if (c > 0 && np <= 16 * c) break;
+      const v4f v[2] = {g.acc[0][c], g.acc[1][c]};
+      float s[2];
+      reduce<2>(red, v, s);
+      const int j = 16 * c + tid / 16;
+      if (j < np) {
+        const float a = act_mul<kActSilu>(s[0], s[1]) * r.w[start + j];
+        static_cast<Half<TY>*>(p.act)[(size_t)(start + j) * F + ct * 16 + tid % 16] = (Half<TY>)a;
+      }
+    }
+    it += gridDim.x;
+    if (it >= items) break;
+    n = -1;  // the next item's first stages are on their way
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
+#endif
+}
+
+// hr: rows of H a block.
+template <int TY, int NT>
+__global__ void __launch_bounds__(kThreads, 2) k_few_down(FewArgs p, int hr) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using R = Ring<TY, 1, NT>;
+  __shared__ __align__(1024) uint8_t ring[kWaves * kRingBytes];
+  __shared__ __align__(16) float red[kWaves][1][256];
+  __shared__ FewTable tab;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
+  const int nt = p.tab->n;
+  for (int i = tid; i < nt; i += kThreads) {
+    tab.slot[i] = p.tab->slot[i];
+    tab.start[i] = p.tab->start[i];
+    tab.mask[i] = p.tab->mask[i];
+  }
+  __syncthreads();
+  const int H = p.H, F = p.F, kst = F / kStageK;
+  const int h0 = blockIdx.x * hr, nh = min(hr, H - h0);
+  const int total = nt * kst;
+  const int rounds = (total + kWaves * R::NS - 1) / (kWaves * R::NS);
+  const uint32_t rowb = 2u * (uint32_t)F;
+  uint32_t avo[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+    avo[m] = (lane >> 3) + 8 * m < nh ? (uint32_t)((lane >> 3) + 8 * m) * rowb + dma_piece(lane) : kOob;
+  const rsrc_t ar = make_rsrc(p.act, (uint32_t)(p.T * p.k) * rowb), none = make_rsrc(p.act, 0);
+
+  int i = -1, s = wave + kst;  // the next loads: slot index, stage of it (once advanced: below kst)
+  rsrc_t wr = none;
+  uint32_t bvo[NT];
+  auto advance = [&]() {  // to the stage s of the touched slots' stages in a row
+    if (s < kst) return;
+    while (s >= kst) {
+      s -= kst;
+      ++i;
+    }
+    const bool live = i < nt;
+    const int ii = live ? i : 0;
+    const int slot = __builtin_amdgcn_readfirstlane(live ? (int)tab.slot[ii] : 0);
+    const uint32_t mask = live ? tab.mask[ii] : 0;
+    const int start = live ? tab.start[ii] : 0;
+    wr = make_rsrc(static_cast<const uint8_t*>(p.w2) + ((size_t)slot * H + h0) * rowb, live ? (uint32_t)nh * rowb : 0u);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const int t = 16 * c + l16;
+      bvo[c] = mask >> t & 1 ? (uint32_t)(start + __popc(mask & ((1u << t) - 1))) * rowb + 16u * q : kOob;
+    }
+  };
+  R g;
+#pragma unroll
+  for (int c = 0; c < NT; ++c) g.acc[0][c] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (nt > 0) {
+    advance();
+    auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
+      const uint32_t so = (uint32_t)s * 128u;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo[m], so, 0, 2);
+      const rsrc_t b = i < nt ? ar : none;
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) g.b[u][c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
+      s += kWaves;
+      advance();
+    };
+    auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
+      if (first) {
+#pragma unroll
+        for (int u = 0; u < R::PRE; ++u) issue(to, u);
+        return;
+      }
+#pragma unroll
+      for (int u = 0; u < R::NS; ++u) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((R::PRE - 1) * R::I) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        issue(to, (u + R::PRE) % R::NS);
+        consume<TY, 1, NT>(from + u * R::kSlot, g, u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
+    for (int n = -1; n < rounds; ++n) stages(mine, mine, n < 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
+  }
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const v4f v[1] = {g.acc[0][c]};
+    float o[1];
+    reduce<1>(red, v, o);
+    const int t = 16 * c + tid / 16, h = tid % 16;
+    if (t < p.T && h < nh) static_cast<Half<TY>*>(p.out)[(size_t)t * H + h0 + h] = (Half<TY>)o[0];
+  }
+#endif
+}
+
+constexpr int kBlocks = 512;  // two a compute unit
+
+template <int TY, int NT>
+hipError_t run(const FewArgs& p, hipStream_t st) {
+  const long slots = p.P_local < p.T * p.k ? p.P_local : p.T * p.k;
+  const long items = slots * (p.F / 16);
+  const unsigned up = (unsigned)(items < kBlocks ? items : kBlocks);
+  if (p.E <= 128) k_few_up<TY, NT, 2><<<up, kThreads, 0, st>>>(p);
+  else if (p.E <= 384) k_few_up<TY, NT, 6><<<up, kThreads, 0, st>>>(p);
+  else k_few_up<TY, NT, 16><<<up, kThreads, 0, st>>>(p);
+  // rows a block: what gives every compute unit two blocks, at most a tile of 16
+  const int want = (p.H + kBlocks - 1) / kBlocks, hr = want < 4 ? 4 : want < 16 ? want : 16;
+  k_few_down<TY, NT><<<(unsigned)((p.H + hr - 1) / hr), kThreads, 0, st>>>(p, hr);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t few_table_bytes() { return sizeof(FewTable); }
+
+hipError_t launch_few(int type, const FewArgs& p, hipStream_t st) {
+  if (type == kBF16) return p.T <= 16 ? run<kBF16, 1>(p, st) : run<kBF16, 2>(p, st);
+  return p.T <= 16 ? run<kF16, 1>(p, st) : run<kF16, 2>(p, st);
+}
+
+}  // namespace moe

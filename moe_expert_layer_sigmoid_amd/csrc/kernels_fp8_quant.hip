@@ -12,6 +12,7 @@
 
 #include <type_traits>
 
+#include "act_device.hpp"
 #include "linear_internal.hpp"
 #include "moe_device.hpp"
 
@@ -48,36 +49,6 @@ __device__ __forceinline__ void load_row(const void* p, size_t i, float (&v)[kPe
       }
     }
   }
-}
-
-// e^-g from the hardware's exp2 (1 ulp), its argument carried in two parts:
-// one f32 product -g log2(e) would lose log2|g| bits of the result.
-__device__ __forceinline__ float exp_neg(float g) {
-  const float hi = g * -1.44269504f;
-  const float lo = fmaf(g, -1.44269504f, -hi) + g * -1.92596299e-8f;  // log2(e) = 1.44269504 + 1.92596299e-8
-  return __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.69314718f, 1.0f);
-}
-
-// silu(g) u for g >= kFarGate: the hardware's reciprocal (1 ulp) in place of a
-// division keeps the kernel on the memory's side of its balance (in all within
-// 9 x 2^-24 of the value, far below the codes' 2^-4).  Above 88 the sigmoid
-// rounds to 1, and e^-inf by the two parts above would be NaN.
-constexpr float kFarGate = -80.0f;
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  const float e = exp_neg(g);
-  const float r = g > 88.0f ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e);
-  return g * r * u;
-}
-
-// silu(g) u for g < kFarGate, where 1 + e^-g rounds to e^-g: g e^g u.  Below
-// -87 neither e^g nor its reciprocal is a normal f32, while the product may be
-// one (silu(-88) = -5e-37, times u): t = e^(g/4) is normal down to -349, where
-// no u brings the product back into range, and every partial product is
-// normal wherever the result is (four errors of t and five roundings: 21 x
-// 2^-24).  g = -inf: NaN, as in the formula.
-__device__ __forceinline__ float silu_mul_far(float g, float u) {
-  const float t = exp_neg(-0.25f * g);
-  return (g * t) * (u * t) * t * t;
 }
 
 // One thread per 16 columns, 8 threads per block of 128: every load and store

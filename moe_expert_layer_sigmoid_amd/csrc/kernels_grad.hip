@@ -1,0 +1,249 @@
+// The global norm over many tensors, sqrt(sum of squares), and the tensors
+// scaled by min(1, max_norm / (norm + 1e-6)).
+//
+// Tensors are cut into chunks of kChunkElems values; a launch holds up to
+// kTable tensors in its arguments (no table in memory that could go stale), and
+// its blocks take equal runs of chunks.  A block's sum of squares is one f64
+// partial sum: squares of f32 values keep their range and the sum all the bits
+// that the result can show, whatever the order, and the order is fixed.  Every
+// block of the scaling launch adds the partial sums (a few KB, from L2) itself
+// and walks its run backwards, so that what the first pass read last is read first.
+// Bound by memory.
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "linear_internal.hpp"
+#include "moe_device.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlocks = 2048;        // partial sums of all launches together, and one a launch more
+constexpr int kChunkElems = 8192;
+constexpr int kTable = 112;          // 3.3 KB of arguments, under the 4 KB limit
+
+struct Table {
+  const void* in[kTable];
+  void* out[kTable];
+  int64_t n[kTable];
+  uint32_t end[kTable];  // chunks up to the tensor's end
+  uint8_t type[kTable];
+  int count;
+  int part0;             // the launch's first partial sum
+};
+
+typedef v4i v4i_any __attribute__((aligned(2)));
+
+template <int T>
+using Elem = std::conditional_t<T == kBF16, __bf16, std::conditional_t<T == kF16, _Float16, float>>;
+
+// Calls f(tensor, first element, elements) for the block's chunks, in order or
+// backwards.
+template <class F>
+__device__ __forceinline__ void chunks(const Table& t, bool back, F f) {
+  const uint32_t total = t.end[t.count - 1];
+  const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.x / gridDim.x);
+  const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (c0 == c1) return;
+  const uint32_t first = back ? c1 - 1 : c0;
+  int lo = 0, hi = t.count - 1;  // the first tensor whose end is past `first`
+  while (lo < hi) {
+    const int m = (lo + hi) / 2;
+    if (t.end[m] > first) hi = m;
+    else lo = m + 1;
+  }
+  for (uint32_t k = 0; k < c1 - c0; ++k) {
+    const uint32_t c = back ? first - k : first + k;
+    while (t.end[lo] <= c) ++lo;
+    while (lo > 0 && t.end[lo - 1] > c) --lo;
+    const int64_t e0 = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * kChunkElems;
+    const int64_t left = t.n[lo] - e0;
+    f(lo, e0, (int)(left < kChunkElems ? left : kChunkElems));
+  }
+}
+
+// One chunk, 16 bytes a thread and step: f(values, count, index of the first) for full and partial pieces.
+template <int T, class F>
+__device__ __forceinline__ void pieces(const Elem<T>* p, int n, F f) {
+  constexpr int V = 16 / sizeof(Elem<T>), S = kChunkElems / (V * kThreads);
+  v4i x[S];
+  if (n == kChunkElems) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) x[s] = *reinterpret_cast<const v4i_any*>(p + (s * kThreads + threadIdx.x) * V);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      Elem<T> v[V];
+      __builtin_memcpy(v, &x[s], 16);
+      f(v, V, (s * kThreads + (int)threadIdx.x) * V);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x * V; i < n; i += kThreads * V) {
+    Elem<T> v[V];
+    const int m = min(V, n - i);
+    if (m == V) {
+      const v4i w = *reinterpret_cast<const v4i_any*>(p + i);
+      __builtin_memcpy(v, &w, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = e < m ? p[i + e] : (Elem<T>)0.0f;
+    }
+    f(v, m, i);
+  }
+}
+
+// f on the tensor's type
+template <class F>
+__device__ __forceinline__ void with_type(int type, F f) {
+  if (type == kBF16) f(std::integral_constant<int, kBF16>{});
+  else if (type == kF16) f(std::integral_constant<int, kF16>{});
+  else f(std::integral_constant<int, kF32>{});
+}
+
+// The sum of every thread's value, in every thread.
+__device__ __forceinline__ double block_sum(double s) {
+  __shared__ double red[kThreads / 64];
+#pragma unroll
+  for (int d = 32; d; d /= 2) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64] = s;
+  __syncthreads();
+  s = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) s += red[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_squares(Table t, double* part) {
+  double s = 0.0;
+  chunks(t, false, [&](int i, int64_t e0, int n) {
+    with_type(t.type[i], [&](auto tc) {
+      constexpr int T = decltype(tc)::value;
+      pieces<T>(static_cast<const Elem<T>*>(t.in[i]) + e0, n, [&](const auto& v, int, int) {
+#pragma unroll
+        for (int e = 0; e < (int)(16 / sizeof(v[0])); ++e) {  // past a tensor's end: zeros
+          const double x = (double)(float)v[e];
+          s = fma(x, x, s);
+        }
+      });
+    });
+  });
+  s = block_sum(s);
+  if (threadIdx.x == 0) part[t.part0 + blockIdx.x] = s;
+}
+
+__device__ __forceinline__ double norm_of(const double* part, int parts) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+  return sqrt(block_sum(s));
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const double* part, int parts, float* norm) {
+  const double v = norm_of(part, parts);
+  if (threadIdx.x == 0) *norm = (float)v;
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_scale(Table t, const double* part, int parts, float max_norm,
+                                                         float* norm) {
+  const double v = norm_of(part, parts);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+  const double q = max_norm / (v + 1e-6);
+  // a NaN norm gives NaN, an infinite one 0; a factor near or below f32's normal
+  // range keeps its bits by a power of two apart
+  const float scale = q < 0x1p-64 ? 0x1p-64f : 1.0f;
+  const float c = q > 1.0 ? 1.0f : (float)(q / scale);
+  chunks(t, true, [&](int i, int64_t e0, int n) {
+    if (c == 1.0f && t.in[i] == t.out[i]) return;  // nothing to change
+    with_type(t.type[i], [&](auto tc) {
+      constexpr int T = decltype(tc)::value;
+      using E = Elem<T>;
+      E* out = static_cast<E*>(t.out[i]) + e0;
+      pieces<T>(static_cast<const E*>(t.in[i]) + e0, n, [&](const auto& v, int m, int at) {
+        constexpr int V = 16 / sizeof(E);
+        E x[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = (E)((float)v[e] * c * scale);
+        if (m == V) {
+          v4i w;
+          __builtin_memcpy(&w, x, 16);
+          *reinterpret_cast<v4i_any*>(out + at) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (e < m) out[at + e] = x[e];
+        }
+      });
+    });
+  });
+}
+
+int launches(int count) { return (count + kTable - 1) / kTable; }
+
+// The chunks of a tensor.
+uint64_t chunks_of(const GradTensor& g) { return ((uint64_t)g.n + kChunkElems - 1) / kChunkElems; }
+
+// Calls f(table, blocks) for each launch; returns the number of partial sums.
+template <class F>
+int each_table(const GradTensor* g, int count, F f) {
+  uint64_t all = 0;
+  for (int i = 0; i < count; ++i) all += chunks_of(g[i]);
+  int part = 0;
+  Table t;
+  for (int i = 0; i < count;) {
+    uint32_t total = 0;
+    t.count = 0;
+    for (; i < count && t.count < kTable; ++i) {
+      if (!g[i].n) continue;
+      const int k = t.count++;
+      total += (uint32_t)chunks_of(g[i]);
+      t.in[k] = g[i].in;
+      t.out[k] = g[i].out;
+      t.n[k] = g[i].n;
+      t.type[k] = (uint8_t)g[i].type;
+      t.end[k] = total;
+    }
+    if (!t.count) break;
+    // the launch's share of kBlocks blocks, at least one
+    const uint64_t share = all <= kBlocks ? total : (uint64_t)total * kBlocks / all;
+    const unsigned blocks = (unsigned)(share ? share : 1);
+    t.part0 = part;
+    part += (int)blocks;
+    f(t, blocks);
+  }
+  return part;
+}
+
+}  // namespace
+
+size_t grad_workspace(int count) { return (size_t)(kBlocks + launches(count)) * sizeof(double); }
+
+hipError_t launch_grad_norm(const GradTensor* g, int count, float* norm, void* ws, hipStream_t st) {
+  double* part = static_cast<double*>(ws);
+  const int parts = each_table(g, count, [&](const Table& t, unsigned blocks) {
+    k_grad_squares<<<blocks, kThreads, 0, st>>>(t, part);
+  });
+  k_grad_norm<<<1, kThreads, 0, st>>>(part, parts, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const GradTensor* g, int count, float max_norm, float* norm, void* ws, hipStream_t st) {
+  double* part = static_cast<double*>(ws);
+  const int parts = each_table(g, count, [&](const Table& t, unsigned blocks) {
+    k_grad_squares<<<blocks, kThreads, 0, st>>>(t, part);
+  });
+  if (!parts) {  // no values: norm 0
+    if (norm) k_grad_norm<<<1, kThreads, 0, st>>>(part, 0, norm);
+    return hipGetLastError();
+  }
+  bool first = true;
+  each_table(g, count, [&](const Table& t, unsigned blocks) {
+    k_grad_scale<<<blocks, kThreads, 0, st>>>(t, part, parts, max_norm, first ? norm : nullptr);
+    first = false;
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -533,6 +533,36 @@ size_t moe_a16w4_workspace_bytes(const moe_dims_t* d) {
   return layout_of(d).total + round_up((size_t)d->T_max * d->k * d->F * 2, kAlign);
 }
 
+size_t moe_a16w16_workspace_bytes(const moe_dims_t* d) {
+  if (check_dims(d) != MOE_OK) return 0;
+  const size_t rows = (size_t)(d->T_max < kFewMaxT ? d->T_max : kFewMaxT) * d->k;
+  return round_up(few_table_bytes(), kAlign) + round_up(rows * d->F * 2, kAlign);
+}
+
+int moe_forward_a16w16(const moe_dims_t* d, int32_t type, const int32_t* num_tokens, const void* x, const float* logits,
+                       const void* w1, const void* w2, const int32_t* rep_count, const int32_t* rep_slots,
+                       int32_t* load_hist, void* out, const moe_taps_t* taps, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  int rc = check_dims(d);
+  if (rc) return rc;
+  if (type != MOE_TYPE_BF16 && type != MOE_TYPE_F16) return MOE_ERR_INVALID_ARG;
+  const auto rows_ok = [&](const void* p) { return d->T == 0 ? opt_ok(p) : dev_ok(p); };  // no tokens, no tensors
+  if (!rows_ok(x) || !rows_ok(logits) || !dev_ok(w1) || !dev_ok(w2) || !dev_ok(rep_count) || !dev_ok(rep_slots) ||
+      !opt_ok(load_hist) || !rows_ok(out) || ((uintptr_t)num_tokens & 3))
+    return MOE_ERR_INVALID_ARG;
+  if (taps && (!opt_ok(taps->topk_ids) || !opt_ok(taps->topk_w) || !opt_ok(taps->phys_ids))) return MOE_ERR_INVALID_ARG;
+  if (d->T > kFewMaxT) return MOE_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < moe_a16w16_workspace_bytes(d)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws % kAlign) != 0) return MOE_ERR_INVALID_ARG;
+  if (d->T == 0) return MOE_OK;
+  const moe_taps_t none{};
+  const moe_taps_t& tp = taps ? *taps : none;
+  const FewArgs p{x, logits, w1, w2, rep_count, rep_slots, num_tokens, load_hist, out, tp.topk_ids, tp.topk_w,
+                  tp.phys_ids, at<void>(ws, round_up(few_table_bytes(), kAlign)), at<FewTable>(ws, 0), d->T, d->H, d->F,
+                  d->E, d->k, d->P_total, d->p0, d->P_local, d->R_max, d->token_id_base};
+  return hip_status(launch_few(type, p, (hipStream_t)stream));
+}
+
 int moe_forward_a16w4(const moe_dims_t* d, const uint16_t* x, const float* logits, const uint8_t* pw1,
                       const uint8_t* pw1s, const uint8_t* pw2, const uint8_t* pw2s, const int32_t* rep_count,
                       const int32_t* rep_slots, int32_t* load_hist, uint16_t* out, const moe_taps_t* taps,

@@ -172,4 +172,27 @@ hipError_t launch_gemm2_a16_pairs(const uint16_t* act, int T, int k, const int32
                                   int stride, const uint8_t* pw2, const uint8_t* pw2s, float* y, int H, int F,
                                   int P_local, hipStream_t st);
 
+// The layer on 16-bit experts for T <= kFewMaxT tokens (kernels_a16w16.hip), type
+// 0 bf16 or 1 f16: w1 [P_local, 2F, H], w2 [P_local, H, F].  act: T k rows of F
+// values; tab: few_table_bytes().  t_dev, load_hist, ids, wts, phys may be null.
+constexpr int kFewMaxT = 32;
+struct FewTable;
+struct FewArgs {
+  const void* x;
+  const float* logits;
+  const void *w1, *w2;
+  const int32_t *rep_count, *rep_slots, *t_dev;
+  int32_t* load_hist;
+  void* out;
+  int32_t* ids;
+  float* wts;
+  int32_t* phys;
+  void* act;
+  FewTable* tab;
+  int T, H, F, E, k, P_total, p0, P_local, R_max;
+  uint32_t base;
+};
+size_t few_table_bytes();
+hipError_t launch_few(int type, const FewArgs& p, hipStream_t st);
+
 }  // namespace moe
