@@ -570,7 +570,7 @@ _bind_module = None
 
 class _PythonChecks:
     """In place of _bind: launches nothing."""
-    quant = fp8 = grouped = staticmethod(lambda *a: None)
+    quant = fp8 = grouped = linear_act = act_backward = grad_clip = layer = staticmethod(lambda *a: None)
 
 
 def _short():
@@ -582,6 +582,8 @@ def _short():
             built = getattr(_bind, "torch_version", "of unknown version")
             if built != str(torch.__version__):
                 raise ImportError(f"it was built for torch {built}, this is {torch.__version__}")
+            if not hasattr(_bind, "layer"):
+                raise ImportError("it was built from older sources")
             _bind_module = _bind
         except ImportError as e:
             warnings.warn(f"linear calls take longer on the host, _bind cannot be used: {e}; build it with "
@@ -774,6 +776,11 @@ def moe_grouped_linear_act(d: Linear, x, w, y, scratch, act: str = "none", gated
     "gelu", "gelu_tanh".  x, w and bias of d's in_type, y, residual and pre of
     its out_type.  ``residual`` may be y; ``pre`` [rows, N] receives z."""
     a = _act(act)
+    rc = _short().linear_act(d, x, w, y, scratch, a, bool(gated), bias, residual, pre, offsets, stream)
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        raise MoeError("moe_grouped_linear_act", rc)
     dev = _device(y, "y")
     t, o = _TORCH_TYPES[d.in_type], _TORCH_TYPES[d.out_type]
     n = d.rows * (d.N // 2 if gated else d.N)
@@ -789,6 +796,11 @@ def moe_grouped_linear_act_backward(d: Linear, dy, pre, dz, scratch, act: str = 
     (its out_type), through the activation; ``db`` float32 [groups, N] receives
     the bias's gradient (zeros for an empty group)."""
     a = _act(act)
+    rc = _short().act_backward(d, dy, pre, dz, scratch, a, bool(gated), db, offsets, stream)
+    if rc == MOE_OK:
+        return
+    if rc is not None:
+        raise MoeError("moe_grouped_linear_act_backward", rc)
     dev = _device(dz, "dz")
     o = _TORCH_TYPES[d.out_type]
     _launch("moe_grouped_linear_act_backward", dev, stream, ctypes.byref(d), a, int(bool(gated)),
@@ -816,6 +828,7 @@ class GradList:
             raise ValueError(f"outs: {len(self.outs)} tensors for {len(self.grads)}")
         self.device = -1
         self._array = (_Tensor * max(len(self.grads), 1))()
+        self.address = ctypes.addressof(self._array)
         spans = []
         for i, (g, o) in enumerate(zip(self.grads, self.outs)):
             name = f"grads[{i}]"
@@ -862,7 +875,7 @@ def _grad(fn: str, grads: GradList, norm, scratch, stream, *args) -> None:
     if not isinstance(grads, GradList):
         raise TypeError("grads: expected a GradList")
     dev = grads.device if len(grads) else _device(scratch, "workspace")
-    _launch(fn, dev, stream, ctypes.addressof(grads._array), len(grads), *args, _opt(norm, "norm", f32, 1, dev),
+    _launch(fn, dev, stream, grads.address, len(grads), *args, _opt(norm, "norm", f32, 1, dev),
             *_scratch(scratch, dev))
 
 
@@ -874,6 +887,12 @@ def moe_grad_norm(grads: GradList, norm, scratch, stream=None) -> None:
 def moe_grad_clip(grads: GradList, max_norm: float, norm, scratch, stream=None) -> None:
     """The list's outs = its grads times min(1, max_norm / (norm + 1e-6)); ``norm``
     (float32 [1] or None) receives the norm before."""
+    if isinstance(grads, GradList):
+        rc = _short().grad_clip(grads.address, len(grads.grads), max_norm, norm, scratch, grads.device, stream)
+        if rc == MOE_OK:
+            return
+        if rc is not None:
+            raise MoeError("moe_grad_clip", rc)
     _grad("moe_grad_clip", grads, norm, scratch, stream, float(max_norm))
 
 
@@ -896,6 +915,12 @@ def moe_forward_a16w16(d: Dims, x, logits, w1, w2, rep_count, rep_slots, out, ws
     ``num_tokens`` (int32 device tensor, one element): the step's token count,
     read by the kernels, for captured graphs.  ``taps``: topk_ids, topk_w,
     phys_ids."""
+    if taps is None:
+        rc = _short().layer(d, x, logits, w1, w2, rep_count, rep_slots, out, ws, num_tokens, load_hist, stream)
+        if rc == MOE_OK:
+            return
+        if rc is not None:
+            raise MoeError("moe_forward_a16w16", rc)
     dev = _device(out, "out")
     if not isinstance(x, torch.Tensor) or x.dtype not in _TORCH_TYPES[:2]:
         raise TypeError("x: expected a bfloat16 or float16 torch.Tensor")

@@ -67,38 +67,61 @@ __device__ __forceinline__ float act_mul(float g, float u) {
   else return g * u;
 }
 
-// act'(z) v.
-//  silu:      s (1 + z (1 - s)), s = sigmoid(z); far below 0, e^z (1 + z)
-//  gelu:      Phi(z) + z phi(z)
-//  gelu_tanh: s + z s (1 - s) 2 w'(z), s = sigmoid(2 w), w' = sqrt(2 / pi) (1 + 3 0.044715 z^2);
-//             beyond 16 it is 1 or 0 in f32, and z^2 would overflow
+// act(z) and act'(z) together, from one exponential:
+//  silu:      s = sigmoid(z): z s and s (1 + z (1 - s)), 1 - s = e s
+//  gelu:      z Phi(z) and Phi(z) + z phi(z)
+//  gelu_tanh: s = sigmoid(t), t = 2 w: z s and s + z s (1 - s) t'(z); beyond 16 the
+//             slope is 1 or 0 in f32, and z^2 would overflow
+// For z >= far_below<ACT>(); below, e^t leaves f32's normal range while a
+// product with it may not: grad_far.
 template <int ACT>
-__device__ __forceinline__ float slope_mul(float z, float v) {
+__device__ __forceinline__ void act_slope(float z, float& f, float& d) {
   if constexpr (ACT == kActRelu) {
-    return z <= 0.0f ? 0.0f : v;
+    f = z < 0.0f ? 0.0f : z;
+    d = z <= 0.0f ? 0.0f : 1.0f;
   } else if constexpr (ACT == kActSilu) {
-    if (z < kFarGate) {
-      const float t = exp_neg(z < -400.0f ? 100.0f : -0.25f * z);
-      return ((1.0f + z) * t) * (v * t) * t * t;
-    }
     const float e = z > 88.0f ? 0.0f : exp_neg(z), s = __builtin_amdgcn_rcpf(1.0f + e);
-    return s * fmaf(z, e * s, 1.0f) * v;  // 1 - s = e s
+    f = z * s;
+    d = s * fmaf(z, e * s, 1.0f);
   } else if constexpr (ACT == kActGelu) {
-    const float h = 0.5f * z * z;
-    return fmaf(z, 0.398942280f * exp_neg(h > 200.0f ? 200.0f : h), 0.5f * erfcf(z * -0.707106781f)) * v;
+    const float h = 0.5f * z * z, c = 0.5f * erfcf(z * -0.707106781f);
+    f = z * c;
+    d = fmaf(z, 0.398942280f * exp_neg(h > 200.0f ? 200.0f : h), c);
   } else if constexpr (ACT == kActGeluTanh) {
     const float x = z > 16.0f ? 16.0f : z < -16.0f ? -16.0f : z;
     const float x2 = x * x, t = 2.0f * kGeluC * x * fmaf(kGeluA, x2, 1.0f);
     const float e = t > 88.0f ? 0.0f : exp_neg(t < -80.0f ? -80.0f : t), s = __builtin_amdgcn_rcpf(1.0f + e);
-    return s * fmaf(x * (e * s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f) * v;
+    f = z * s;
+    d = s * fmaf(x * (e * s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f);
   } else {
-    return v;
+    f = z;
+    d = 1.0f;
+  }
+}
+template <int ACT>
+constexpr float far_below() {
+  return ACT == kActSilu ? kFarGate : ACT == kActGeluTanh ? -9.0f : -__builtin_inff();
+}
+
+// dz and df for z < far_below<ACT>(): v act'(z) and w act(z), e^t in four factors
+// (silu: act' = e^z (1 + z); gelu_tanh: e^t (1 + z t'(z)); 1 - s is 1 there).
+template <int ACT>
+__device__ __forceinline__ void grad_far(float z, float v, float w, float& dz, float& df) {
+  if constexpr (ACT == kActSilu) {
+    const float t = exp_neg(z < -400.0f ? 100.0f : -0.25f * z);
+    dz = ((1.0f + z) * t) * (v * t) * t * t;
+    df = (z * t) * (w * t) * t * t;
+  } else if constexpr (ACT == kActGeluTanh) {
+    const float x = z < -20.0f ? -20.0f : z, x2 = x * x;  // t(-20) = -603: zero
+    const float t = exp_neg(-0.5f * kGeluC * x * fmaf(kGeluA, x2, 1.0f));
+    dz = (fmaf(x * 2.0f * kGeluC, fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f) * t) * (v * t) * t * t;
+    df = (x * t) * (w * t) * t * t;
   }
 }
 
 // f(std::integral_constant<int, act>) for a runtime act.
 template <class F>
-__device__ __forceinline__ void with_act(int act, F f) {
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
   if (act == kActSilu) f(std::integral_constant<int, kActSilu>{});
   else if (act == kActRelu) f(std::integral_constant<int, kActRelu>{});
   else if (act == kActGelu) f(std::integral_constant<int, kActGelu>{});

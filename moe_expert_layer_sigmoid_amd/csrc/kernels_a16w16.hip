@@ -22,8 +22,8 @@
 #include <type_traits>
 
 #include "act_device.hpp"
-#include "linear_kernel.hpp"
 #include "moe_internal.hpp"
+#include "ring.hpp"
 #include "route_device.hpp"
 
 namespace moe {
@@ -41,25 +41,7 @@ struct FewTable {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
-constexpr int kRingBytes = 16384;      // of a wave
-constexpr int kStageK = 64;            // reduction elements of a stage: 128 bytes of a row
-
-// A wave's ring: NA tiles of 16 weight rows a stage, NS stages, and the token
-// operands of those stages in registers.
-template <int TY, int NA, int NT>
-struct Ring {
-  static constexpr int kSlot = NA * 2048;
-  static constexpr int NS = kRingBytes / kSlot, PRE = NS - 1;
-  static constexpr int I = 2 * NA + 2 * NT;  // loads of a stage
-  static_assert((PRE - 1) * I < 63, "vmcnt range");
-  v4i b[NS][NT][2];
-  v4f acc[NA][NT];
-};
-
-template <int TY>
-using Half = std::conditional_t<TY == kBF16, __bf16, _Float16>;
+constexpr int kThreads = kRingThreads, kWaves = kRingWaves;
 
 // ---- routing: the block's view of all tokens -------------------------------
 struct Routed {
@@ -156,45 +138,6 @@ __device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScra
     r.w[row] = w;
   }
   __syncthreads();
-}
-
-// ---- one stage --------------------------------------------------------------
-// Lane offsets of the DMA: 8 rows of 128 bytes an instruction, the 16-byte pieces
-// of a row permuted so that the reads spread over the LDS banks.
-__device__ __forceinline__ uint32_t dma_piece(int lane) { return 16u * (uint32_t)((lane & 7) ^ (lane >> 3)); }
-
-template <int TY, int NA, int NT>
-__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT>& g, int u) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const v4i w = *reinterpret_cast<const lds_v4i*>(rd + a * 2048 + l16 * 128 + (((4 * kk + q) ^ (l16 & 7)) * 16));
-#pragma unroll
-      for (int c = 0; c < NT; ++c) g.acc[a][c] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c]);
-    }
-}
-
-// The waves' sums of acc[a][c], by thread (token column tid / 16, weight row tid % 16).
-template <int NA>
-__device__ __forceinline__ void reduce(float (*red)[NA][256], const v4f (&v)[NA], float (&s)[NA]) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-#pragma unroll
-  for (int a = 0; a < NA; ++a) *reinterpret_cast<v4f*>(&red[wave][a][(lane & 15) * 16 + 4 * (lane >> 4)]) = v[a];
-  // (LDS alone is waited for: the loads of the next stages stay in flight)
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int a = 0; a < NA; ++a) {
-    s[a] = red[0][a][tid];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) s[a] += red[w][a][tid];
-  }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 template <int TY, int NT, int EPL>

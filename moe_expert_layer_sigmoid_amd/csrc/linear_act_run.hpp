@@ -4,7 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "linear_kernel.hpp"
+#include "linear_rows.hpp"
 
 namespace moe {
 namespace {
@@ -17,15 +17,25 @@ hipError_t run_shape(const LinearArgs& p, const Plan& pl, hipStream_t st) {
 }
 
 template <int IN, int EP>
+hipError_t run_rows(int out_type, const LinearArgs& p, bool big, hipStream_t st) {
+  const int nct = ceil_div(p.N / (EP == kGated ? 2 : 1), 16);
+  const long items = (long)p.rows * nct;  // at most: a row tile a row
+  const auto launch = [&](auto w) {
+    constexpr int W = decltype(w)::value, kMost = 2 * kCus * kRingWaves / W;
+    const unsigned blocks = (unsigned)(items < kMost ? items : kMost);
+    if (big) k_linear_rows<IN, EP, true, W><<<blocks, W * 64, 0, st>>>(p, nct, out_type);
+    else k_linear_rows<IN, EP, false, W><<<blocks, W * 64, 0, st>>>(p, nct, out_type);
+  };
+  if ((p.rows < p.groups ? p.rows : p.groups) * nct <= kCus) launch(std::integral_constant<int, 8>{});
+  else launch(std::integral_constant<int, 4>{});
+  return hipGetLastError();
+}
+
+template <int IN, int EP>
 hipError_t run_ep(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   constexpr int OP = kFwd, G = EP == kGated ? 2 : 1;
   const bool big = streams(IN, p.rows, p.N, p.K, p.groups);
-  if (few_rows(p.rows, p.N / G, p.groups)) {
-    const dim3 grid((unsigned)ceil_div(p.N / G, 16), p.groups);
-    if (big) k_linear_few<IN, true, EP><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
-    else k_linear_few<IN, false, EP><<<grid, kFewWaves * 64, 0, st>>>(p, out_type);
-    return hipGetLastError();
-  }
+  if (p.rows <= kRowsMax) return run_rows<IN, EP>(out_type, p, big, st);
   // (a gated tile of TA columns makes TA / 2 outputs: as many tiles as the plain product's)
   Choice c = choose(OP, IN, p.rows, p.N, p.K, p.groups);
   c.plan.out_type = out_type;
@@ -40,8 +50,8 @@ hipError_t run_ep(int out_type, LinearArgs p, void* ws, hipStream_t st) {
   else if (c.shape == 5) e = run_shape<Shape<IN, OP, 128, 32, 2, 2, 1, 3, 2>, EP>(p, c.plan, st);
   else e = run_shape<Shape<IN, OP, 256, 192, 2, 4, 1, 2, 1>, EP>(p, c.plan, st);
   if (e != hipSuccess || c.plan.splits == 1) return e;
-  const size_t want = ((size_t)p.rows * ceil_div(p.N / G, 4) + 255) / 256;
-  const unsigned blocks = (unsigned)(want < 2048 ? want : 2048);
+  const long want = ((long)p.rows * ceil_div(p.N / G, 256) + 3) / 4;
+  const unsigned blocks = (unsigned)(want < 4096 ? want : 4096);
   if (out_type == kF32) k_linear_join_act<kF32, IN, EP><<<blocks, 256, 0, st>>>(p, c.plan.splits);
   else k_linear_join_act<IN, IN, EP><<<blocks, 256, 0, st>>>(p, c.plan.splits);
   return hipGetLastError();

@@ -42,7 +42,6 @@ struct ActBackwardArgs {
   float* db;
   int rows, N, groups, act;
 };
-constexpr int kActBackwardRows = 64;  // rows of one group that a block adds up
 size_t act_backward_workspace(int rows, int N, int groups);
 hipError_t launch_act_backward(int in_type, int out_type, bool gated, const ActBackwardArgs& p, void* ws, hipStream_t st);
 

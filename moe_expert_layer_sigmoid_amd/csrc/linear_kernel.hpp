@@ -697,19 +697,16 @@ constexpr int kFewWaves = 8;
 constexpr int kChunk = 4;
 
 // NT: the weights with the streaming policy (one row, 4096 x 7168 in fp8, cached:
-// 1.2 us longer with it than the 7.9 without).  Gated: 16 gate and 16 up columns a
-// block.
-template <int IN, bool NT, int EP = kPlain>
+// 1.2 us longer with it than the 7.9 without).
+template <int IN, bool NT>
 __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int out_type) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int ES = IN == kFP8 ? 1 : 2;
-  constexpr int G = EP == kGated ? 2 : 1;
-  __shared__ __align__(16) float red[kFewWaves][G * 256];
+  __shared__ __align__(16) float red[kFewWaves][256];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
   const int g = blockIdx.y, c0 = blockIdx.x * 16;
-  const int n_out = p.N / G;
   int lo, hi;
   group_rows(p.off, g, p.rows, lo, hi);  // p.rows <= 16
   if (hi == lo) return;
@@ -718,29 +715,14 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
   const int npc = (int)(rowb + 127) / 128;  // 128-byte pieces of a row
   const int nkb = (p.K + 127) / 128, nnb = (p.N + 127) / 128;
   const rsrc_t Ar = make_rsrc(static_cast<const uint8_t*>(p.a) + ((size_t)g * p.N + c0) * rowb,
-                              (uint32_t)(G == 2 ? p.N - c0 : min(16, p.N - c0)) * rowb);
+                              (uint32_t)min(16, p.N - c0) * rowb);
   const rsrc_t Br = make_rsrc(static_cast<const uint8_t*>(p.b) + (size_t)lo * rowb, (uint32_t)nr * rowb);
   const rsrc_t Sr = make_rsrc(IN == kFP8 ? p.bs + (size_t)lo * nkb : nullptr, IN == kFP8 ? (uint32_t)(nr * nkb) * 4u : 0u);
   const rsrc_t Tr = make_rsrc(IN == kFP8 ? p.as + ((size_t)g * nnb + c0 / 128) * nkb : nullptr,
                               IN == kFP8 ? (uint32_t)nkb * 4u : 0u);
-  // the output element of this thread, and what its epilogue adds: on its way during the product
-  const int r = tid >> 4, c = c0 + (tid & 15);
-  const bool mine = r < nr && c < n_out;
-  const size_t at = (size_t)(lo + r) * n_out + c;
-  float bias[G] = {}, res = 0.0f;
-  if constexpr (EP != kPlain) {
-    using B = std::conditional_t<IN == kBF16, __bf16, _Float16>;
-    if (mine && p.bias) {
-#pragma unroll
-      for (int h = 0; h < G; ++h) bias[h] = (float)static_cast<const B*>(p.bias)[(size_t)g * p.N + h * n_out + c];
-    }
-    if (mine && p.res) res = out_type == kF32 ? static_cast<const float*>(p.res)[at] : (float)static_cast<const B*>(p.res)[at];
-  }
-  v4f acc[G];
-#pragma unroll
-  for (int t = 0; t < G; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
   struct Piece {
-    v4i a[G][2], b[2];
+    v4i a[2], b[2];
     int xs, ws;
   };
   Piece buf[2][kChunk];
@@ -751,8 +733,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t at = o + 64u * h < rowb ? (uint32_t)l16 * rowb + o + 64u * h : kOob;
-#pragma unroll
-      for (int t = 0; t < G; ++t) x.a[t][h] = buf_load16_p<NT ? 2 : 0>(Ar, at, (uint32_t)(t * n_out) * rowb);
+      x.a[h] = buf_load16_p<NT ? 2 : 0>(Ar, at, 0);
       x.b[h] = buf_load16(Br, at, 0);
     }
     if constexpr (IN == kFP8) {
@@ -763,16 +744,14 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
   auto add = [&](const Piece& x) {
     if constexpr (IN == kFP8) {
       const float s = __int_as_float(x.xs) * __int_as_float(x.ws);
-      const v8i a = __builtin_shufflevector(x.a[0][0], x.a[0][1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const v8i a = __builtin_shufflevector(x.a[0], x.a[1], 0, 1, 2, 3, 4, 5, 6, 7);
       const v8i b = __builtin_shufflevector(x.b[0], x.b[1], 0, 1, 2, 3, 4, 5, 6, 7);
       const v4f d = mfma8(a, b, v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[0][e] = fmaf(d[e], s, acc[0][e]);
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(d[e], s, acc[e]);
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < G; ++t) acc[t] = mfma16<IN>(x.a[t][h], x.b[h], acc[t]);
+      for (int h = 0; h < 2; ++h) acc = mfma16<IN>(x.a[h], x.b[h], acc);
     }
   };
 #pragma unroll
@@ -787,33 +766,17 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_linear_few(LinearArgs p, int
       for (int k = 0; k < kChunk; ++k) add(buf[h][k]);
     }
   }
-#pragma unroll
-  for (int t = 0; t < G; ++t) *reinterpret_cast<v4f*>(&red[wave][t * 256 + l16 * 16 + 4 * q]) = acc[t];
+  *reinterpret_cast<v4f*>(&red[wave][l16 * 16 + 4 * q]) = acc;
   __syncthreads();
-  if (!mine) return;
-  float z[G];
+  const int r = tid >> 4, c = c0 + (tid & 15);
+  if (r < nr && c < p.N) {
+    float s = red[0][tid];
 #pragma unroll
-  for (int t = 0; t < G; ++t) {
-    z[t] = red[0][t * 256 + tid];
-#pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) z[t] += red[w][t * 256 + tid];
-  }
-  auto put = [&](void* out, size_t i, float v) {
-    if (out_type == kF32) static_cast<float*>(out)[i] = v;
-    else if (out_type == kF16) static_cast<_Float16*>(out)[i] = (_Float16)v;
-    else static_cast<__bf16*>(out)[i] = (__bf16)v;
-  };
-  if constexpr (EP == kPlain) {
-    put(p.out, at, z[0]);
-  } else {
-#pragma unroll
-    for (int t = 0; t < G; ++t) {
-      z[t] += bias[t];
-      if (p.pre) put(p.pre, (size_t)(lo + r) * p.N + t * n_out + c, z[t]);
-    }
-    float v = 0.0f;
-    with_act(p.act, [&](auto a) { v = act_mul<decltype(a)::value>(z[0], G == 2 ? z[G - 1] : 1.0f); });
-    put(p.out, at, v + res);
+    for (int w = 1; w < kFewWaves; ++w) s += red[w][tid];
+    const size_t o = (size_t)(lo + r) * p.N + c;
+    if (out_type == kF32) static_cast<float*>(p.out)[o] = s;
+    else if (out_type == kF16) static_cast<_Float16*>(p.out)[o] = (_Float16)s;
+    else static_cast<__bf16*>(p.out)[o] = (__bf16)s;
   }
 #endif
 }
@@ -851,71 +814,102 @@ __global__ void __launch_bounds__(256) k_linear_join(LinearArgs p, int rows, int
   }
 }
 
-// The same with the epilogue (OUT: the output's type, B: the bias's), four output
-// columns a thread.  A row's group, for its bias, is the last whose offset is not
-// past it.
+// The same with the epilogue (OUT: the output's type, IN: the bias's), four output
+// columns a thread and one row a wave, so that the row's group is one load and a
+// ballot away.  (77 rows x 1021 gated columns, 3 splits: 5.3 us; with a binary
+// search a thread and the bounds of the rows in groups loaded first 8.1.)
 template <int OUT, int IN, int EP>
 __global__ void __launch_bounds__(256) k_linear_join_act(LinearArgs p, int splits) {
 #ifdef __HIP_DEVICE_COMPILE__
   using O = std::conditional_t<OUT == kBF16, __bf16, std::conditional_t<OUT == kF16, _Float16, float>>;
   using B = std::conditional_t<IN == kBF16, __bf16, _Float16>;
   constexpr int G = EP == kGated ? 2 : 1;
-  const int n_out = p.N / G;
-  const uint32_t quads = (uint32_t)(n_out + 3) / 4;
+  const int n_out = p.N / G, across = (n_out + 255) / 256;  // waves a row
   const size_t pitch = (size_t)((p.N + 3) & ~3), total = (size_t)p.rows * pitch;
-  size_t i0 = 0, i1 = (size_t)p.rows * quads;
-  if (p.off) {
-    i0 = (size_t)min(max(p.off[0], 0), p.rows) * quads;
-    i1 = (size_t)min(max(p.off[p.groups], 0), p.rows) * quads;
-  }
   const float* part = static_cast<const float*>(p.part);
-  for (size_t i = i0 + (size_t)blockIdx.x * 256 + threadIdx.x; i < i1; i += (size_t)gridDim.x * 256) {
-    const size_t row = i / quads;
-    const int c = (int)(i - row * quads) * 4, nc = min(4, n_out - c);
-    int g = 0;
-    if (p.off && p.bias) {
-      int hi = p.groups;  // off[g] <= row < off[hi]
-      while (hi - g > 1) {
-        const int m = (g + hi) / 2;
-        if (p.off[m] <= (int)row) g = m;
-        else hi = m;
+  const int lane = threadIdx.x & 63;
+  const long waves = (long)p.rows * across;
+  for (long i = (long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < waves; i += (long)gridDim.x * 4) {
+    const int row = (int)(i / across), c = (int)(i % across) * 256 + 4 * lane, nc = min(4, n_out - c);
+    // n of four values of type X
+    auto get = [&](const auto* s, float (&o)[4]) {
+      using X = std::decay_t<decltype(*s)>;
+      X x[4];
+      if (nc == 4) {
+        typedef X v4x __attribute__((ext_vector_type(4), aligned(sizeof(X))));
+        const v4x w = *reinterpret_cast<const v4x*>(s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = e < nc ? s[e] : (X)0.0f;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = (float)x[e];
+    };
+    auto put = [&](O* o, const float (&v)[4]) {
+      if (nc == 4) {
+        typedef O v4x __attribute__((ext_vector_type(4), aligned(sizeof(O))));
+        v4x w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = (O)v[e];
+        *reinterpret_cast<v4x*>(o) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < nc) o[e] = (O)v[e];
+      }
+    };
+    // the first splits' sums, of both halves, and the residual are on their way
+    // while the row's group is looked for
+    const float* s = part + row * pitch + c;
+    float x[4][G][4], z[G][4], bias[G][4] = {}, res[4] = {}, v[4];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int h = 0; h < G; ++h) get(s + (size_t)min(t + k, splits - 1) * total + h * n_out, x[k][h]);
+    };
+    fetch(0);
+    if (p.res) get(static_cast<const O*>(p.res) + (size_t)row * n_out + c, res);
+    // the row's group: the number of groups that end at or before it; past the last, or
+    // before the first: in none
+    int g = 0;
+    bool in = true;
+    if (p.off) {
+      in = row >= p.off[0] && row < p.off[p.groups];
+      for (int k = 0; k < p.groups; k += 64)
+        g += __popcll(__ballot(k + lane < p.groups && p.off[min(k + lane, p.groups - 1) + 1] <= row));
+      g = min(g, p.groups - 1);
     }
-    float z[G][4], v[4];
+    if (p.bias) {
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      const float* s = part + row * pitch + h * n_out + c;
+      for (int h = 0; h < G; ++h) get(static_cast<const B*>(p.bias) + (size_t)g * p.N + h * n_out + c, bias[h]);
+    }
+    for (int t = 0;;) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[h][e] = e < nc ? s[e] : 0.0f;
-      for (int t = 1; t < splits; t += 4) {
-        float x[4][4];
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[k][e] = e < nc ? s[(size_t)min(t + k, splits - 1) * total + e] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int h = 0; h < G; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (t + k < splits) z[h][e] += x[k][e];
-      }
+            if (t + k < splits) z[h][e] = t + k == 0 ? x[k][h][e] : z[h][e] + x[k][h][e];
+      if ((t += 4) >= splits) break;
+      fetch(t);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < nc) {
-          if (p.bias) z[h][e] += (float)static_cast<const B*>(p.bias)[(size_t)g * p.N + h * n_out + c + e];
-          if (p.pre) static_cast<O*>(p.pre)[row * p.N + h * n_out + c + e] = (O)z[h][e];
-        }
+    for (int h = 0; h < G; ++h) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[h][e] += bias[h][e];
+      if (p.pre && in) put(static_cast<O*>(p.pre) + (size_t)row * p.N + h * n_out + c, z[h]);
     }
     with_act(p.act, [&](auto a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act_mul<decltype(a)::value>(z[0][e], G == 2 ? z[G - 1][e] : 1.0f);
     });
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < nc) {
-        const size_t at = row * n_out + c + e;
-        static_cast<O*>(p.out)[at] = (O)(p.res ? v[e] + (float)static_cast<const O*>(p.res)[at] : v[e]);
-      }
+    for (int e = 0; e < 4; ++e) v[e] += res[e];
+    if (in) put(static_cast<O*>(p.out) + (size_t)row * n_out + c, v);
   }
 #endif
 }
