@@ -2,20 +2,18 @@
 //   k_few_up    routing and remap of every token in every block (a token's logits
 //               are 1.5 KB in L2, a launch more costs longer); then, for 16
 //               columns of F of a touched slot, h = W1 x and
-//               act = round(w_tj silu(gate) up), the token's routing weight w_tj
-//               folded in before the one rounding to the operands' type (as the
-//               layer's other 16-bit variant rounds act; the sum over a token's
-//               experts then needs no second pass);
-//   k_few_down  out[t] = sum over the touched slots of W2 act: a block owns up to
-//               16 rows of H for all tokens and all slots, so that sums stay in
+//               act = w_tj silu(gate) up, the token's routing weight folded in, so
+//               that the sum over a token's experts needs no second pass;
+//   k_few_down  out[t] = sum over the touched slots of W2 act: a block owns a few
+//               rows of H for all tokens and all slots, so that sums stay in
 //               f32 accumulators from the first slot to the last and nothing is
 //               joined in memory.
+// act goes from one to the other as two numbers of the operands' type whose sum is
+// the f32 value to twice the type's bits: rounded once, it would bring as much
+// error as the output's own rounding (normwise 0.0024 for 0.0017 in bf16), and the
+// matrix instructions have time to spare.
 // MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
-// experts' weights, read once; whole 128-byte lines go by DMA into an LDS ring that
-// belongs to one wave alone, with every 4th stage of the reduction its own, so that no wave waits
-// for another but at the end of a block's columns, and the next columns' weights
-// are then already on their way.  x and act rows (a few KB, from L2) are loaded
-// straight into the operand registers as far ahead.
+// experts' weights, streamed as ring.hpp says.
 
 #include <hip/hip_runtime.h>
 
@@ -30,8 +28,10 @@ namespace moe {
 
 constexpr int kPairs = kFewMaxT * 16;  // T k at most
 
-// The touched slots, ascending; their pairs are rows [start, start + popc(mask)),
-// one per bit (token) of mask, ascending.
+// The touched slots, ascending; the pairs of an entry are act rows [start, start +
+// popc(mask)), one per bit (token) of mask, ascending.  A slot with more than 16 tokens
+// is two entries (its weights are then read twice, the second time mostly from
+// a cache; a second tile of tokens for every slot cost the others 6 %).
 struct FewTable {
   int n;
   int pad[3];
@@ -106,22 +106,31 @@ __device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScra
     int nt = 0, rows = 0;
     for (int c = 0; c < p.P_local; c += 64) {
       const uint32_t m = c + lane < p.P_local ? s.mask[c + lane] : 0;
-      const unsigned long long any = __ballot(m != 0);
-      int pre = __popc(m);
+      const int np = __popc(m);
+      int pre = np | (np > 16 ? 2 : np > 0 ? 1 : 0) << 16;  // pairs, and entries above them
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const int up = __shfl_up(pre, d);
         if (lane >= d) pre += up;
       }
       if (m) {
-        const int i = nt + __popcll(any & ((1ull << lane) - 1));
+        const int end = nt + (pre >> 16), i = end - (np > 16 ? 2 : 1), r0 = rows + (pre & 0xFFFF) - np;
+        uint32_t rest = m;  // without its first 16 tokens
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) rest &= rest - 1;
         s.before[c + lane] = i;
         r.tab.slot[i] = (uint16_t)(c + lane);
-        r.tab.start[i] = (uint16_t)(rows + pre - __popc(m));
-        r.tab.mask[i] = m;
+        r.tab.start[i] = (uint16_t)r0;
+        r.tab.mask[i] = m ^ rest;
+        if (rest) {
+          r.tab.slot[i + 1] = (uint16_t)(c + lane);
+          r.tab.start[i + 1] = (uint16_t)(r0 + 16);
+          r.tab.mask[i + 1] = rest;
+        }
       }
-      nt += __popcll(any);
-      rows += __builtin_amdgcn_readlane(pre, 63);
+      const int all = __builtin_amdgcn_readlane(pre, 63);
+      nt += all >> 16;
+      rows += all & 0xFFFF;
     }
     if (lane == 0) r.tab.n = nt;
   }
@@ -140,10 +149,10 @@ __device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScra
   __syncthreads();
 }
 
-template <int TY, int NT, int EPL>
+template <int TY, int EPL>
 __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
-  using R = Ring<TY, 2, NT>;
+  using R = Ring<TY, 2, 1>;
   __shared__ __align__(1024) uint8_t ring[kWaves * kRingBytes];
   __shared__ __align__(16) float red[kWaves][2][256];
   __shared__ Routed r;
@@ -160,8 +169,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
       p.tab->mask[i] = r.tab.mask[i];
     }
   }
+  // Items: 16 columns of an entry, dealt to the blocks in turn.  (Equal shares to the
+  // column, the last part of a block's narrower, were slower: 388 us for 371 at
+  // 43 slots, 60 for 57 at 6.  A narrow part has as many stages, of fewer bytes in flight.)
   const int H = p.H, F = p.F, nct = F / 16;
   const int items = __builtin_amdgcn_readfirstlane(r.tab.n) * nct;
+  if ((int)blockIdx.x >= items) return;  // fewer slots touched than pairs: the same in the whole block
   const int kst = H / kStageK;
   const int rounds = (kst + kWaves * R::NS - 1) / (kWaves * R::NS);
   const uint32_t rowb = 2u * (uint32_t)H;
@@ -171,19 +184,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
   // where the next loads come from
   int item = blockIdx.x, round = 0;
   rsrc_t wr = none;
-  uint32_t wso = 0, xvo[NT];
-  auto seek = [&]() {  // of `item`
+  uint32_t wso = 0, xvo = kOob;
+  auto seek = [&]() {
     const bool live = item < items;
     const int i = live ? item / nct : 0, ct = live ? item - i * nct : 0;
     const int slot = __builtin_amdgcn_readfirstlane((int)r.tab.slot[i]);
     const int start = r.tab.start[i], n = live ? __popc(r.tab.mask[i]) : 0;
-    wr = make_rsrc(static_cast<const uint8_t*>(p.w1) + (live ? (size_t)slot * 2 * F * rowb : 0), live ? 2u * (uint32_t)F * rowb : 0u);
+    wr = make_rsrc(static_cast<const uint8_t*>(p.w1) + (size_t)slot * 2 * F * rowb, live ? 2u * (uint32_t)F * rowb : 0u);
     wso = (uint32_t)ct * 16u * rowb;
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int j = 16 * c + l16;
-      xvo[c] = j < n ? (uint32_t)r.tok[start + j] * rowb + 16u * q : kOob;
-    }
+    xvo = l16 < n ? (uint32_t)r.tok[start + l16] * rowb + 16u * q : kOob;
   };
   R g;
   auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
@@ -196,9 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo,
                                                so + wso + ((m & 1) * 8u + (m >> 1) * (uint32_t)F) * rowb, 0, 2);
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) g.b[u][c][kk] = buf_load16(x, xvo[c], so + 64u * kk);
+    for (int kk = 0; kk < 2; ++kk) g.b[u][0][kk] = buf_load16(x, xvo, so + 64u * kk);
   };
   // NS stages; before the first, the loads alone.  to and from are the same ring,
   // as __restrict__: the compiler then places no wait of its own between a DMA in
@@ -222,37 +229,45 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
         }
       }
       issue(to, (u + R::PRE) % R::NS);
-      consume<TY, 2, NT>(from + u * R::kSlot, g, u);
+      consume(from + u * R::kSlot, g, u);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
-  if ((int)blockIdx.x >= items) return;  // fewer slots touched than pairs: the same in the whole block
+  const auto clear = [&]() { g.acc[0][0] = g.acc[1][0] = v4f{0.f, 0.f, 0.f, 0.f}; };
+  const auto finish = [&](int it) {
+    const int i = it / nct, ct = it - i * nct;
+    const int start = r.tab.start[i], np = __popc(r.tab.mask[i]);
+    const v4f v[2] = {g.acc[0][0], g.acc[1][0]};
+    float s[2];
+    reduce<2>(red, v, s);
+    const int j = tid / 16;
+    if (j < np) {
+      using T = Half<TY>;
+      const float a = act_mul<kActSilu>(s[0], s[1]) * r.w[start + j];
+      const T hi = (T)a;
+      const float rest = a - (float)hi;
+      T* const o = static_cast<T*>(p.act) + (size_t)(start + j) * F + ct * 16 + tid % 16;
+      o[0] = hi;
+      o[(size_t)p.T * p.k * F] = (T)(fabsf((float)hi) == INFINITY ? 0.0f : rest);  // (f16 past its range: infinite)
+    }
+  };
+  if (const int per = (kst + kWaves - 1) / kWaves; per <= R::PRE) {  // short: one burst an item
+    for (; item < items; item += gridDim.x) {
+      clear();
+      seek();
+      burst<R>(mine, per, issue, g);
+      finish(item);
+    }
+    return;
+  }
   seek();
   int it = blockIdx.x;  // the item being added up
   for (int n = -1;; ++n) {
-    if (n <= 0) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) g.acc[a][c] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
+    if (n <= 0) clear();
     stages(mine, mine, n < 0);
     if (n + 1 < rounds) continue;
-    const int i = it / nct, ct = it - i * nct;
-    const int start = r.tab.start[i], np = __popc(r.tab.mask[i]);
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      if (c > 0 && np <= 16 * c) break;
-      const v4f v[2] = {g.acc[0][c], g.acc[1][c]};
-      float s[2];
-      reduce<2>(red, v, s);
-      const int j = 16 * c + tid / 16;
-      if (j < np) {
-        const float a = act_mul<kActSilu>(s[0], s[1]) * r.w[start + j];
-        static_cast<Half<TY>*>(p.act)[(size_t)(start + j) * F + ct * 16 + tid % 16] = (Half<TY>)a;
-      }
-    }
+    finish(it);
     it += gridDim.x;
     if (it >= items) break;
     n = -1;  // the next item's first stages are on their way
@@ -261,18 +276,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
 #endif
 }
 
-// hr: rows of H a block.
-template <int TY, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_few_down(FewArgs p, int hr) {
+// hr <= 16 NA: rows of H a block.
+constexpr int kDownWaves = 8;
+template <int TY, int NA, int NT>
+__global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int hr) {
 #ifdef __HIP_DEVICE_COMPILE__
-  using R = Ring<TY, 1, NT>;
-  __shared__ __align__(1024) uint8_t ring[kWaves * kRingBytes];
-  __shared__ __align__(16) float red[kWaves][1][256];
+  using R = Ring<TY, NA, NT, 2>;
+  constexpr int W = kDownWaves;
+  __shared__ __align__(1024) uint8_t ring[W * kRingBytes];
+  __shared__ __align__(16) float red[W][NA][256];
   __shared__ FewTable tab;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int nt = p.tab->n;
-  for (int i = tid; i < nt; i += kThreads) {
+  for (int i = tid; i < nt; i += W * 64) {
     tab.slot[i] = p.tab->slot[i];
     tab.start[i] = p.tab->start[i];
     tab.mask[i] = p.tab->mask[i];
@@ -281,18 +298,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_down(FewArgs p, int hr) {
   const int H = p.H, F = p.F, kst = F / kStageK;
   const int h0 = blockIdx.x * hr, nh = min(hr, H - h0);
   const int total = nt * kst;
-  const int rounds = (total + kWaves * R::NS - 1) / (kWaves * R::NS);
+  const int rounds = (total + W * R::NS - 1) / (W * R::NS);
   const uint32_t rowb = 2u * (uint32_t)F;
-  uint32_t avo[2];
+  uint32_t avo[2 * NA];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int m = 0; m < 2 * NA; ++m)
     avo[m] = (lane >> 3) + 8 * m < nh ? (uint32_t)((lane >> 3) + 8 * m) * rowb + dma_piece(lane) : kOob;
-  const rsrc_t ar = make_rsrc(p.act, (uint32_t)(p.T * p.k) * rowb), none = make_rsrc(p.act, 0);
+  // act: T k rows, and the second numbers' rows behind them
+  const uint32_t half = (uint32_t)(p.T * p.k) * rowb;
+  const rsrc_t ar = make_rsrc(p.act, 2 * half), none = make_rsrc(p.act, 0);
 
-  int i = -1, s = wave + kst;  // the next loads: slot index, stage of it (once advanced: below kst)
+  int i = -1, s = wave + kst;  // the next loads: entry, stage of it (once advanced: below kst)
   rsrc_t wr = none;
   uint32_t bvo[NT];
-  auto advance = [&]() {  // to the stage s of the touched slots' stages in a row
+  auto advance = [&]() {  // to stage s of the entries' stages in a row
     if (s < kst) return;
     while (s >= kst) {
       s -= kst;
@@ -312,20 +331,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_down(FewArgs p, int hr) {
   };
   R g;
 #pragma unroll
-  for (int c = 0; c < NT; ++c) g.acc[0][c] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int a = 0; a < NA; ++a)
+#pragma unroll
+    for (int c = 0; c < NT; ++c) g.acc[a][c] = v4f{0.f, 0.f, 0.f, 0.f};
   if (nt > 0) {
     advance();
     auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
       const uint32_t so = (uint32_t)s * 128u;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2 * NA; ++m)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo[m], so, 0, 2);
       const rsrc_t b = i < nt ? ar : none;
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) g.b[u][c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
-      s += kWaves;
+        for (int kk = 0; kk < 2; ++kk) {
+          g.b[u][2 * c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
+          g.b[u][2 * c + 1][kk] = buf_load16(b, bvo[c] + half, so + 64u * kk);  // (kOob + half: still past every buffer)
+        }
+      s += W;
       advance();
     };
     auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
@@ -339,38 +363,49 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_down(FewArgs p, int hr) {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((R::PRE - 1) * R::I) : "memory");
         __builtin_amdgcn_sched_barrier(0);
         issue(to, (u + R::PRE) % R::NS);
-        consume<TY, 1, NT>(from + u * R::kSlot, g, u);
+        consume(from + u * R::kSlot, g, u);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
-    for (int n = -1; n < rounds; ++n) stages(mine, mine, n < 0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
+    if (const int per = (total + W - 1) / W; per <= R::PRE) {
+      burst<R>(mine, per, issue, g);
+    } else {
+      for (int n = -1; n < rounds; ++n) stages(mine, mine, n < 0);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
+    }
   }
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    const v4f v[1] = {g.acc[0][c]};
-    float o[1];
-    reduce<1>(red, v, o);
-    const int t = 16 * c + tid / 16, h = tid % 16;
-    if (t < p.T && h < nh) static_cast<Half<TY>*>(p.out)[(size_t)t * H + h0 + h] = (Half<TY>)o[0];
+    v4f v[NA];
+    float o[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) v[a] = g.acc[a][c];
+    reduce<NA, W>(red, v, o);
+    const int t = 16 * c + tid / 16;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const int h = 16 * a + tid % 16;
+      if (tid < 256 && t < p.T && h < nh) static_cast<Half<TY>*>(p.out)[(size_t)t * H + h0 + h] = (Half<TY>)o[a];
+    }
   }
 #endif
 }
 
-constexpr int kBlocks = 512;  // two a compute unit
-
-template <int TY, int NT>
+template <int TY>
 hipError_t run(const FewArgs& p, hipStream_t st) {
-  const long slots = p.P_local < p.T * p.k ? p.P_local : p.T * p.k;
-  const long items = slots * (p.F / 16);
-  const unsigned up = (unsigned)(items < kBlocks ? items : kBlocks);
-  if (p.E <= 128) k_few_up<TY, NT, 2><<<up, kThreads, 0, st>>>(p);
-  else if (p.E <= 384) k_few_up<TY, NT, 6><<<up, kThreads, 0, st>>>(p);
-  else k_few_up<TY, NT, 16><<<up, kThreads, 0, st>>>(p);
-  // rows a block: what gives every compute unit two blocks, at most a tile of 16
-  const int want = (p.H + kBlocks - 1) / kBlocks, hr = want < 4 ? 4 : want < 16 ? want : 16;
-  k_few_down<TY, NT><<<(unsigned)((p.H + hr - 1) / hr), kThreads, 0, st>>>(p, hr);
+  const long slots = (long)p.P_local * (p.T > 16 ? 2 : 1), pairs = (long)p.T * p.k;
+  const long items = (slots < pairs ? slots : pairs) * (p.F / 16);
+  const unsigned up = (unsigned)(items < 2 * kCus ? items : 2 * kCus);
+  if (p.E <= 128) k_few_up<TY, 2><<<up, kThreads, 0, st>>>(p);
+  else if (p.E <= 384) k_few_up<TY, 6><<<up, kThreads, 0, st>>>(p);
+  else k_few_up<TY, 16><<<up, kThreads, 0, st>>>(p);
+  // rows a block: what gives every compute unit one block, at least 4, at most two tiles of 16
+  const int want = (p.H + kCus - 1) / kCus, hr = want < 4 ? 4 : want < 32 ? want : 32;
+  const unsigned down = (unsigned)((p.H + hr - 1) / hr);
+  if (p.T > 16) k_few_down<TY, 2, 2><<<down, kDownWaves * 64, 0, st>>>(p, hr);
+  else if (hr > 16) k_few_down<TY, 2, 1><<<down, kDownWaves * 64, 0, st>>>(p, hr);
+  else k_few_down<TY, 1, 1><<<down, kDownWaves * 64, 0, st>>>(p, hr);
   return hipGetLastError();
 }
 
@@ -379,8 +414,7 @@ hipError_t run(const FewArgs& p, hipStream_t st) {
 size_t few_table_bytes() { return sizeof(FewTable); }
 
 hipError_t launch_few(int type, const FewArgs& p, hipStream_t st) {
-  if (type == kBF16) return p.T <= 16 ? run<kBF16, 1>(p, st) : run<kBF16, 2>(p, st);
-  return p.T <= 16 ? run<kF16, 1>(p, st) : run<kF16, 2>(p, st);
+  return type == kBF16 ? run<kBF16>(p, st) : run<kF16>(p, st);
 }
 
 }  // namespace moe

@@ -18,15 +18,15 @@ hipError_t run_shape(const LinearArgs& p, const Plan& pl, hipStream_t st) {
 
 template <int IN, int EP>
 hipError_t run_rows(int out_type, const LinearArgs& p, bool big, hipStream_t st) {
-  const int nct = ceil_div(p.N / (EP == kGated ? 2 : 1), 16);
-  const long items = (long)p.rows * nct;  // at most: a row tile a row
+  const int live = p.rows < p.groups ? p.rows : p.groups;
+  const long cols = (long)live * (p.N / (EP == kGated ? 2 : 1)), shares = (cols + kRowsLeastCols - 1) / kRowsLeastCols;
   const auto launch = [&](auto w) {
     constexpr int W = decltype(w)::value, kMost = 2 * kCus * kRingWaves / W;
-    const unsigned blocks = (unsigned)(items < kMost ? items : kMost);
-    if (big) k_linear_rows<IN, EP, true, W><<<blocks, W * 64, 0, st>>>(p, nct, out_type);
-    else k_linear_rows<IN, EP, false, W><<<blocks, W * 64, 0, st>>>(p, nct, out_type);
+    const unsigned blocks = (unsigned)(shares < kMost ? shares : kMost);
+    if (big) k_linear_rows<IN, EP, true, W><<<blocks, W * 64, 0, st>>>(p, out_type);
+    else k_linear_rows<IN, EP, false, W><<<blocks, W * 64, 0, st>>>(p, out_type);
   };
-  if ((p.rows < p.groups ? p.rows : p.groups) * nct <= kCus) launch(std::integral_constant<int, 8>{});
+  if (cols <= 16 * kCus) launch(std::integral_constant<int, 8>{});
   else launch(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }

@@ -1,8 +1,8 @@
 // The product with its epilogue for at most 16 rows in all: the weights of the
 // groups with rows are streamed once, every sum is finished in its block, nothing
-// is joined in memory.  Items are 16 output columns of a group (gated: 16 gate and
-// 16 up columns), dealt to blocks that stay; W waves a block: eight where the items
-// are no more than the compute units, else four, twice a unit.  Bound by the weights and by
+// is joined in memory.  A block takes an equal share of the groups' output columns, 16
+// at a time (gated: 16 gate and 16 up columns); W waves a block: eight, one block a
+// compute unit, where that gives a unit 16 columns at most, else four and two.  Bound by the weights and by
 // the latency of one burst.  (One row, 4096 x 7168, gated: 13.7 us, 18.0 by a block's
 // eight waves loading weights into registers; 512 x 7168 plain 8.7 and 11.0; 1024 x
 // 1024 gated 6.3, by tiles 7.6.  More rows a group read x too often for that: 48 rows,
@@ -15,10 +15,11 @@ namespace moe {
 namespace {
 
 constexpr int kRowsMax = 16;
+constexpr int kRowsLeastCols = 4;  // of a block
 
 // BIG: the weights pass the caches (the streaming policy, as in k_linear)
 template <int IN, int EP, bool BIG, int W>
-__global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int nct, int out_type) {
+__global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out_type) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int G = EP == kGated ? 2 : 1;
   using R = Ring<IN, G, 1>;
@@ -29,36 +30,45 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int nct
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int n_out = p.N / G;
   const RowTiles<kRowsMax> rt(p.off, p.groups, p.rows);  // a tile is a group with rows
-  const int items = rt.total * nct;
-  if ((int)blockIdx.x >= items) return;
+  const int cols = rt.total * n_out;
+  const int share = max(kRowsLeastCols, (cols + (int)gridDim.x - 1) / (int)gridDim.x);
+  int at = blockIdx.x * share;  // of the columns being added up
+  const int end = min(cols, at + share);
+  if (at >= end) return;
   const uint32_t rowb = 2u * (uint32_t)p.K;
   const int kst = (int)((rowb + 127) / 128);
   const int rounds = (kst + W * R::NS - 1) / (W * R::NS);
 
-  struct Item {
-    int g, c0, r0, nr;
+  // Columns [c0, c0 + n) of a group and its rows, from column `col` of the row.
+  struct Part {
+    int g, c0, n, r0, nr;
   };
-  auto find = [&](int item) {
+  auto part = [&](int col) {
     int g, t, lo, hi;
-    rt.find(item / nct, g, t, lo, hi);
-    return Item{g, item % nct * 16, lo, hi - lo};
+    rt.find(col / n_out, g, t, lo, hi);
+    const int c0 = col % n_out;
+    return Part{g, c0, min(16, min(n_out - c0, end - col)), lo, hi - lo};
   };
 
   const rsrc_t none = make_rsrc(p.a, 0);
-  const uint32_t kpc = dma_piece(lane);
-  int item = blockIdx.x, round = 0;  // the next loads
+  int next = at, round = 0;  // the next loads
   rsrc_t wr = none, xr = none;
-  // Row offsets of the DMA instructions: 8 rows each, then the up columns.  All in
-  // the checked offset: rows past the matrix (gated: past the group's weights) give zeros.
+  // Row offsets of the DMA instructions: 8 rows each, then the up columns.
+  const uint32_t kpc = dma_piece(lane);
   uint32_t avo[2 * G];
-#pragma unroll
-  for (int m = 0; m < 2 * G; ++m) avo[m] = (uint32_t)((m & 1) * 8 + (lane >> 3) + (m >> 1) * n_out) * rowb + kpc;
   const uint32_t xvo = (uint32_t)l16 * rowb + 16u * q;
+  int len = 0;
   auto seek = [&]() {
-    const bool live = item < items;
-    const Item x = find(live ? item : items - 1);
+    const bool live = next < end;
+    const Part x = part(live ? next : at);
+    len = x.n;
     wr = make_rsrc(static_cast<const uint8_t*>(p.a) + ((size_t)x.g * p.N + x.c0) * rowb, live ? (uint32_t)(p.N - x.c0) * rowb : 0u);
     xr = make_rsrc(static_cast<const uint8_t*>(p.b) + (size_t)x.r0 * rowb, live ? (uint32_t)x.nr * rowb : 0u);
+#pragma unroll
+    for (int m = 0; m < 2 * G; ++m) {
+      const int row = (m & 1) * 8 + (lane >> 3);
+      avo[m] = row < x.n ? (uint32_t)(row + (m >> 1) * n_out) * rowb + kpc : kOob;
+    }
   };
   R g;
   auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
@@ -66,7 +76,7 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int nct
     const bool in = so + kpc < rowb;  // not so for pieces past the row's end and stages past the last
 #pragma unroll
     for (int m = 0; m < 2 * G; ++m)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void)(to + u * R::kSlot + m * 1024), 16, in ? avo[m] + so : kOob, 0, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void)(to + u * R::kSlot + m * 1024), 16, in && avo[m] != kOob ? avo[m] + so : kOob, 0, 0,
                                                BIG ? 2 : 0);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
@@ -89,43 +99,38 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int nct
       if (u == 1) {  // the loads enter the next round
         if (++round == rounds) {
           round = 0;
-          item += gridDim.x;
+          next += len;
           seek();
         }
       }
       issue(to, (u + R::PRE) % R::NS);
-      consume<IN, G, 1>(from + u * R::kSlot, g, u);
+      consume(from + u * R::kSlot, g, u);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
-  seek();
-  int it = blockIdx.x;  // the item being added up
-  for (int n = -1;; ++n) {
-    if (n <= 0) {
+  const auto clear = [&]() {
 #pragma unroll
-      for (int a = 0; a < G; ++a) g.acc[a][0] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
-    stages(mine, mine, n < 0);
-    if (n + 1 < rounds) continue;
-    const Item x = find(it);
+    for (int a = 0; a < G; ++a) g.acc[a][0] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  const auto finish = [&](const Part& x) {
     const int j = tid / 16, col = x.c0 + tid % 16;
-    const bool here = j < x.nr && col < n_out;  // (nr <= 16: the first four waves)
-    const size_t row = (size_t)(x.r0 + j), at = row * n_out + col;
+    const bool here = j < x.nr && tid % 16 < x.n;  // (nr <= 16: the first four waves)
+    const size_t row = (size_t)(x.r0 + j), o = row * n_out + col;
     float bias[G] = {}, res = 0.0f;
     if (p.bias && here) {
 #pragma unroll
       for (int h = 0; h < G; ++h) bias[h] = (float)static_cast<const B*>(p.bias)[(size_t)x.g * p.N + h * n_out + col];
     }
-    if (p.res && here) res = out_type == kF32 ? static_cast<const float*>(p.res)[at] : (float)static_cast<const B*>(p.res)[at];
+    if (p.res && here) res = out_type == kF32 ? static_cast<const float*>(p.res)[o] : (float)static_cast<const B*>(p.res)[o];
     v4f v[G];
     float z[G], y = 0.0f;
 #pragma unroll
     for (int a = 0; a < G; ++a) v[a] = g.acc[a][0];
     reduce<G, W>(red, v, z);
-    auto put = [&](void* out, size_t i, float o) {
-      if (out_type == kF32) static_cast<float*>(out)[i] = o;
-      else static_cast<B*>(out)[i] = (B)o;
+    auto put = [&](void* out, size_t i, float e) {
+      if (out_type == kF32) static_cast<float*>(out)[i] = e;
+      else static_cast<B*>(out)[i] = (B)e;
     };
     if (here) {
 #pragma unroll
@@ -134,11 +139,31 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int nct
         if (p.pre) put(p.pre, row * p.N + h * n_out + col, z[h]);
       }
       with_act(p.act, [&](auto a) { y = act_mul<decltype(a)::value>(z[0], G == 2 ? z[G - 1] : 1.0f); });
-      put(p.out, at, y + res);
+      put(p.out, o, y + res);
     }
-    it += gridDim.x;
-    if (it >= items) break;
-    n = -1;  // the next item's first stages are on their way
+  };
+  if (const int per = (kst + W - 1) / W; per <= R::PRE) {  // short: one burst a part
+    while (at < end) {
+      const Part x = part(at);
+      clear();
+      next = at;
+      seek();
+      burst<R>(mine, per, issue, g);
+      finish(x);
+      at += x.n;
+    }
+    return;
+  }
+  seek();
+  for (int n = -1;; ++n) {
+    if (n <= 0) clear();
+    stages(mine, mine, n < 0);
+    if (n + 1 < rounds) continue;
+    const Part x = part(at);
+    finish(x);
+    at += x.n;
+    if (at >= end) break;
+    n = -1;  // the next columns' first stages are on their way
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
 #endif

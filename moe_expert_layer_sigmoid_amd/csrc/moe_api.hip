@@ -536,7 +536,7 @@ size_t moe_a16w4_workspace_bytes(const moe_dims_t* d) {
 size_t moe_a16w16_workspace_bytes(const moe_dims_t* d) {
   if (check_dims(d) != MOE_OK) return 0;
   const size_t rows = (size_t)(d->T_max < kFewMaxT ? d->T_max : kFewMaxT) * d->k;
-  return round_up(few_table_bytes(), kAlign) + round_up(rows * d->F * 2, kAlign);
+  return round_up(few_table_bytes(), kAlign) + round_up(rows * d->F * 4, kAlign);
 }
 
 int moe_forward_a16w16(const moe_dims_t* d, int32_t type, const int32_t* num_tokens, const void* x, const float* logits,

@@ -24,14 +24,15 @@ template <int TY>
 using Half = std::conditional_t<TY == kBF16, __bf16, _Float16>;
 
 // A wave's ring: NA tiles of 16 weight rows a stage, NS stages, and the token
-// operands of those stages in registers.
-template <int TY, int NA, int NT>
+// operands of those stages in registers: NT tiles of 16 tokens, each held in P parts
+// whose sum is the value.
+template <int TY, int NA, int NT, int P = 1>
 struct Ring {
   static constexpr int kSlot = NA * 2048;
   static constexpr int NS = kRingBytes / kSlot, PRE = NS - 1;
-  static constexpr int I = 2 * NA + 2 * NT;  // loads of a stage
+  static constexpr int I = 2 * NA + 2 * NT * P;  // loads of a stage
   static_assert((PRE - 1) * I < 63, "vmcnt range");
-  v4i b[NS][NT][2];
+  v4i b[NS][NT * P][2];
   v4f acc[NA][NT];
 };
 
@@ -40,8 +41,8 @@ struct Ring {
 // of a row permuted so that the reads spread over the LDS banks.
 __device__ __forceinline__ uint32_t dma_piece(int lane) { return 16u * (uint32_t)((lane & 7) ^ (lane >> 3)); }
 
-template <int TY, int NA, int NT>
-__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT>& g, int u) {
+template <int TY, int NA, int NT, int P>
+__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT, P>& g, int u) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk)
@@ -49,8 +50,23 @@ __device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT>& g, i
     for (int a = 0; a < NA; ++a) {
       const v4i w = *reinterpret_cast<const lds_v4i*>(rd + a * 2048 + l16 * 128 + (((4 * kk + q) ^ (l16 & 7)) * 16));
 #pragma unroll
-      for (int c = 0; c < NT; ++c) g.acc[a][c] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c]);
+      for (int c = 0; c < NT * P; ++c) g.acc[a][c / P] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c / P]);
     }
+}
+
+// All of a wave's `per` <= PRE stages in one burst: short reductions, where a full
+// ring would wait for stages that are not there (the tiny layer: 5.8 + 7.5 us for
+// TINY0 + TINY1).
+template <class R, class Issue>
+__device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, R& g) {
+#pragma unroll
+  for (int u = 0; u < R::PRE; ++u)
+    if (u < per) issue(mine, u);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int u = 0; u < R::PRE; ++u)
+    if (u < per) consume(mine + u * R::kSlot, g, u);
 }
 
 // The W waves' sums of acc[a][c], by thread of the first four waves (token column

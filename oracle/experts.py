@@ -138,8 +138,9 @@ def clip(grads, max_norm):
 
 def layer(x, w1, w2, phys, topk_w, p0, eps):
     """The layer on the pairs (t, j) of phys / topk_w [T, k]: (out, its bound
-    before the output's rounding).  eps: of the operands' type, to which w * act is
-    rounded; topk_w: float64 weights, 4e-6 of their value uncertain."""
+    before the output's rounding).  eps: of the operands' type, in two numbers of
+    which w * act is held (half a step of the second: eps^2 / 4, and half of f16's
+    smallest number); topk_w: float64 weights, 4e-6 of their value uncertain."""
     T, H = x.shape
     F = w2.shape[2]
     out, tol, mag = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
@@ -156,8 +157,8 @@ def layer(x, w1, w2, phys, topk_w, p0, eps):
             f, w = act("silu", a), topk_w[t, j]
             v = f * u * w
             tv = w * (1.1 * th[:F] * (np.abs(u) + th[F:]) + np.abs(f) * th[F:]) + (24 * U + 4e-6) * np.abs(v)
-            tv += eps / 2 * (np.abs(v) + tv) + 2.0 ** -25   # f16 below its normal numbers
+            tv += eps * eps / 4 * (np.abs(v) + tv) + 2.0 ** -25
             out[t] += w2[s] @ v
             tol[t] += np.abs(w2[s]) @ tv
             mag[t] += np.abs(w2[s]) @ (np.abs(v) + tv)
-    return out, tol + ol.sum_bound(F * max(pairs, 1)) * mag
+    return out, tol + ol.sum_bound(2 * F * max(pairs, 1)) * mag
