@@ -33,10 +33,11 @@ template <int T>
 struct Raw {
   static constexpr int W = sizeof(Elem<T>) / 2;  // 16-byte words
   v4i w[W];
-  __device__ __forceinline__ void load(const Elem<T>* p, int n) {
+  __device__ __forceinline__ void load(const Elem<T>* p, int n, bool once) {
     if (n == kV) {
+      const v4i_any* q = reinterpret_cast<const v4i_any*>(p);
 #pragma unroll
-      for (int h = 0; h < W; ++h) w[h] = load16(reinterpret_cast<const char*>(p) + 16 * h);
+      for (int h = 0; h < W; ++h) w[h] = once ? __builtin_nontemporal_load(q + h) : q[h];
     } else {
       Elem<T> x[kV];
 #pragma unroll
@@ -53,7 +54,7 @@ struct Raw {
 };
 
 template <int T>
-__device__ __forceinline__ void store8(Elem<T>* p, int n, const float (&v)[kV]) {
+__device__ __forceinline__ void store8(Elem<T>* p, int n, bool once, const float (&v)[kV]) {
   static_assert(T != kF32, "16 bytes");
   Elem<T> x[kV];
 #pragma unroll
@@ -61,7 +62,8 @@ __device__ __forceinline__ void store8(Elem<T>* p, int n, const float (&v)[kV]) 
   if (n == kV) {
     v4i w;
     __builtin_memcpy(&w, x, 16);
-    store16(p, w);
+    if (once) __builtin_nontemporal_store(w, reinterpret_cast<v4i_any*>(p));
+    else store16(p, w);
   } else {
 #pragma unroll
     for (int e = 0; e < kV; ++e)
@@ -102,7 +104,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int groups, int ro
 // per: threads across the columns of a block; ncb blocks across; len: rows of a
 // tile, 0 for a group a block.  sums: the partial sums [tile][N], or db itself (len 0).
 template <int IN, int PT, int EP, int ACT>
-__global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBackwardArgs p, int per, int ncb, int len, float* sums) {
+__global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBackwardArgs p, int per, int ncb, int len, bool once, float* sums) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int G = EP == kGated ? 2 : 1;
   constexpr int kAhead = PT == kF32 ? 2 : 4;  // rows a thread has in flight
@@ -126,9 +128,9 @@ __global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBack
 #pragma unroll
       for (int m = 0; m < kAhead; ++m) {
         const size_t r = (size_t)min(r0 + m * subs, hi - 1);
-        d[m].load(dy + r * n_out, nc);
+        d[m].load(dy + r * n_out, nc, once);
 #pragma unroll
-        for (int h = 0; h < G; ++h) z[m][h].load(pre + r * p.N + h * n_out, nc);
+        for (int h = 0; h < G; ++h) z[m][h].load(pre + r * p.N + h * n_out, nc, once);
       }
 #pragma unroll
       for (int m = 0; m < kAhead; ++m) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBack
         for (int h = 0; h < G; ++h) {
 #pragma unroll
           for (int e = 0; e < kV; ++e) acc[h][e] += o[h][e];
-          store8<IN>(dz + (size_t)r * p.N + h * n_out, nc, o[h]);
+          store8<IN>(dz + (size_t)r * p.N + h * n_out, nc, once, o[h]);
         }
       }
     }
@@ -248,8 +250,10 @@ hipError_t run(const ActBackwardArgs& p, void* ws, hipStream_t st) {
   const bool whole = p.db && p.rows <= kWhole;
   float* sums = whole ? p.db : p.db ? static_cast<float*>(ws) : nullptr;
   const unsigned blocks = (unsigned)((whole ? p.groups : d.tiles) * d.ncb);
+  // what passes the caches moves with the streaming policy
+  const bool once = (size_t)p.rows * p.N * 4 > kStreamMin;
   const auto launch = [&](auto a) {
-    k_act_backward<IN, PT, EP, decltype(a)::value><<<blocks, kThreads, 0, st>>>(p, d.per, d.ncb, whole ? 0 : d.len, sums);
+    k_act_backward<IN, PT, EP, decltype(a)::value><<<blocks, kThreads, 0, st>>>(p, d.per, d.ncb, whole ? 0 : d.len, once, sums);
   };
   with_act(p.act, launch);
   if (p.db && !whole)

@@ -90,7 +90,7 @@ class Case:
 
 
 SMALL = [(1, 1, 32, 64), (1, 1, 2, 8), (16, 1, 130, 136), (17, 1, 66, 72), (33, 3, 258, 200), (5, 4, 34, 1024),
-         (250, 9, 264, 392), (300, 2, 640, 64)]
+         (250, 9, 264, 392), (300, 2, 640, 64), (10, 100, 68, 80), (16, 16, 48, 3000), (300, 130, 40, 72)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -261,7 +261,7 @@ class Back:
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("act", oe.ACTS)
 @pytest.mark.parametrize("rows,groups,N", [(1, 1, 8), (3, 1, 24), (64, 1, 264), (65, 1, 264), (64, 3, 40), (250, 9, 264),
-                                           (129, 3, 4104), (1000, 5, 2056), (700, 70, 64)])
+                                           (129, 3, 4104), (1000, 5, 2056), (700, 70, 64), (30, 200, 16), (3000, 1000, 16)])
 def test_backward(rows, groups, N, act, gated):
     dt = "f16" if (rows + len(act)) % 2 else "bf16"
     out = "f32" if (rows + len(act)) % 3 == 0 else None
