@@ -17,6 +17,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+
 #include <type_traits>
 
 #include "act_device.hpp"
@@ -41,7 +43,6 @@ struct FewTable {
 
 namespace {
 
-constexpr int kThreads = kRingThreads, kWaves = kRingWaves;
 
 // ---- routing: the block's view of all tokens -------------------------------
 struct Routed {
@@ -57,8 +58,9 @@ struct RouteScratch {
   int rep_slots[1024];
 };
 
-template <int EPL>
+template <int EPL, int W>
 __device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScratch& s) {
+  constexpr int kThreads = W * 64, kWaves = W;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = p.t_dev ? min(max(*p.t_dev, 0), p.T) : p.T;
   const bool flat = p.R_max == 1;  // one replica each: the slots are read beside the logits
@@ -149,19 +151,21 @@ __device__ __forceinline__ void route_all(const FewArgs& p, Routed& r, RouteScra
   __syncthreads();
 }
 
-template <int TY, int EPL>
-__global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
+template <int TY, int EPL, int W>
+__global__ void __launch_bounds__(W * 64, 2) k_few_up(FewArgs p, int ncnt) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int kThreads = W * 64, kWaves = W;
   using R = Ring<TY, 2, 1>;
   __shared__ __align__(1024) uint8_t ring[kWaves * kRingBytes];
   __shared__ __align__(16) float red[kWaves][2][256];
   __shared__ Routed r;
   static_assert(sizeof(RouteScratch) <= sizeof(ring), "scratch in the ring");
-  route_all<EPL>(p, r, *reinterpret_cast<RouteScratch*>(ring));
+  route_all<EPL, W>(p, r, *reinterpret_cast<RouteScratch*>(ring));
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   if (blockIdx.x == 0) {
     const int m = r.tab.n;
+    for (int i = tid; i < ncnt; i += kThreads) p.cnt[i] = 0;
     if (tid == 0) p.tab->n = m;
     for (int i = tid; i < m; i += kThreads) {
       p.tab->slot[i] = r.tab.slot[i];
@@ -240,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
     const int start = r.tab.start[i], np = __popc(r.tab.mask[i]);
     const v4f v[2] = {g.acc[0][0], g.acc[1][0]};
     float s[2];
-    reduce<2>(red, v, s);
-    const int j = tid / 16;
+    reduce<2, W>(red, v, s);
+    const int j = tid / 16;  // (np <= 16: the first four waves)
     if (j < np) {
       using T = Half<TY>;
       const float a = act_mul<kActSilu>(s[0], s[1]) * r.w[start + j];
@@ -276,29 +280,39 @@ __global__ void __launch_bounds__(kThreads, 2) k_few_up(FewArgs p) {
 #endif
 }
 
-// hr <= 16 NA: rows of H a block.
+// hr <= 16 NA: rows of H a block.  Few rows of H leave compute units idle: zs blocks
+// then share a block's entries, as far as every wave gets kLeast stages; each stores its
+// f32 sums, and the last of them to finish (a counter, zeroed by k_few_up) adds
+// them in order.  The sums are stored and loaded device-coherent, past the
+// dies' own L2s, so that completion is all that has to be waited for.
 constexpr int kDownWaves = 8;
+constexpr int kLeast = 4;
 template <int TY, int NA, int NT>
-__global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int hr) {
+__global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int hr, int zs) {
 #ifdef __HIP_DEVICE_COMPILE__
   using R = Ring<TY, NA, NT, 2>;
   constexpr int W = kDownWaves;
   __shared__ __align__(1024) uint8_t ring[W * kRingBytes];
   __shared__ __align__(16) float red[W][NA][256];
   __shared__ FewTable tab;
+  __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int nt = p.tab->n;
+  const int H = p.H, F = p.F, kst = F / kStageK;
+  const int total = nt * kst;  // stages of all entries in a row
+  const int parts = max(1, min(zs, (total + kLeast * W - 1) / (kLeast * W)));
+  const int tile = blockIdx.x / zs, z = blockIdx.x % zs;
+  if (z >= parts) return;
   for (int i = tid; i < nt; i += W * 64) {
     tab.slot[i] = p.tab->slot[i];
     tab.start[i] = p.tab->start[i];
     tab.mask[i] = p.tab->mask[i];
   }
   __syncthreads();
-  const int H = p.H, F = p.F, kst = F / kStageK;
-  const int h0 = blockIdx.x * hr, nh = min(hr, H - h0);
-  const int total = nt * kst;
-  const int rounds = (total + W * R::NS - 1) / (W * R::NS);
+  const int h0 = tile * hr, nh = min(hr, H - h0);
+  const int each = (total + parts - 1) / parts, first = z * each, end = min(total, first + each);
+  const int rounds = (each + W * R::NS - 1) / (W * R::NS);
   const uint32_t rowb = 2u * (uint32_t)F;
   uint32_t avo[2 * NA];
 #pragma unroll
@@ -308,15 +322,11 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
   const uint32_t half = (uint32_t)(p.T * p.k) * rowb;
   const rsrc_t ar = make_rsrc(p.act, 2 * half), none = make_rsrc(p.act, 0);
 
-  int i = -1, s = wave + kst;  // the next loads: entry, stage of it (once advanced: below kst)
+  int at = first + wave;          // the next loads: stage of all,
+  int i = at / kst, s = at % kst;  // entry, stage of it
   rsrc_t wr = none;
   uint32_t bvo[NT];
-  auto advance = [&]() {  // to stage s of the entries' stages in a row
-    if (s < kst) return;
-    while (s >= kst) {
-      s -= kst;
-      ++i;
-    }
+  auto seek = [&]() {  // of entry i
     const bool live = i < nt;
     const int ii = live ? i : 0;
     const int slot = __builtin_amdgcn_readfirstlane(live ? (int)tab.slot[ii] : 0);
@@ -334,14 +344,15 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
   for (int a = 0; a < NA; ++a)
 #pragma unroll
     for (int c = 0; c < NT; ++c) g.acc[a][c] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (nt > 0) {
-    advance();
+  if (first < end) {
+    seek();
     auto issue = [&](lds_u8* to, int u) __attribute__((always_inline)) {
       const uint32_t so = (uint32_t)s * 128u;
+      const bool live = at < end;
+      const rsrc_t w = live ? wr : none, b = live ? ar : none;
 #pragma unroll
       for (int m = 0; m < 2 * NA; ++m)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo[m], so, 0, 2);
-      const rsrc_t b = i < nt ? ar : none;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_void)(to + u * R::kSlot + m * 1024), 16, avo[m], so, 0, 2);
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -349,8 +360,12 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
           g.b[u][2 * c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
           g.b[u][2 * c + 1][kk] = buf_load16(b, bvo[c] + half, so + 64u * kk);  // (kOob + half: still past every buffer)
         }
-      s += W;
-      advance();
+      at += W;
+      if ((s += W) >= kst) {
+        i += s / kst;
+        s %= kst;
+        seek();
+      }
     };
     auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
       if (first) {
@@ -368,13 +383,15 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
       }
     };
     lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
-    if (const int per = (total + W - 1) / W; per <= R::PRE) {
+    if (const int per = (each + W - 1) / W; per <= R::PRE) {
       burst<R>(mine, per, issue, g);
     } else {
       for (int n = -1; n < rounds; ++n) stages(mine, mine, n < 0);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
     }
   }
+  const auto put = [&](int t, int h, float v) { static_cast<Half<TY>*>(p.out)[(size_t)t * H + h0 + h] = (Half<TY>)v; };
+  float* const part = p.part + (size_t)h0 + (size_t)z * p.T * H;
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
     v4f v[NA];
@@ -386,32 +403,93 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const int h = 16 * a + tid % 16;
-      if (tid < 256 && t < p.T && h < nh) static_cast<Half<TY>*>(p.out)[(size_t)t * H + h0 + h] = (Half<TY>)o[a];
+      if (tid < 256 && t < p.T && h < nh) {
+        if (parts == 1) put(t, h, o[a]);
+        else __hip_atomic_store(part + (size_t)t * H + h, o[a], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
   }
+  if (parts == 1) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0)
+    s_last = __hip_atomic_fetch_add(p.cnt + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int e = tid; e < p.T * nh; e += W * 64) {
+    const int t = e / nh, h = e % nh;
+    const float* const o = p.part + (size_t)t * H + h0 + h;
+    float v = 0.0f;
+    for (int k = 0; k < parts; k += 8) {
+      float x[8];
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        x[m] = __hip_atomic_load(o + (size_t)min(k + m, parts - 1) * p.T * H, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        if (k + m < parts) v += x[m];
+    }
+    put(t, h, v);
+  }
 #endif
+}
+
+// How k_few_down is divided: rows of H a block, blocks that share an entry's
+// reduction.  From 2048 rows on, what gives every compute unit one block; below,
+// tiles of 16 rows (32 for two tiles of tokens) and as many blocks a tile as fill the card.
+struct DownPlan {
+  int hr, tiles, zs;
+};
+DownPlan down_plan(int T, int H) {
+  const int whole = T > 16 ? 32 : 16, fit = (H + kCus - 1) / kCus;
+  DownPlan d;
+  d.zs = kCus / ((H + whole - 1) / whole);
+  if (d.zs < 2) d.zs = 1;
+  d.hr = d.zs > 1 ? whole : fit < 32 ? fit : 32;
+  d.tiles = (H + d.hr - 1) / d.hr;
+  return d;
 }
 
 template <int TY>
 hipError_t run(const FewArgs& p, hipStream_t st) {
   const long slots = (long)p.P_local * (p.T > 16 ? 2 : 1), pairs = (long)p.T * p.k;
-  const long items = (slots < pairs ? slots : pairs) * (p.F / 16);
-  const unsigned up = (unsigned)(items < 2 * kCus ? items : 2 * kCus);
-  if (p.E <= 128) k_few_up<TY, 2><<<up, kThreads, 0, st>>>(p);
-  else if (p.E <= 384) k_few_up<TY, 6><<<up, kThreads, 0, st>>>(p);
-  else k_few_up<TY, 16><<<up, kThreads, 0, st>>>(p);
-  // rows a block: what gives every compute unit one block, at least 4, at most two tiles of 16
-  const int want = (p.H + kCus - 1) / kCus, hr = want < 4 ? 4 : want < 32 ? want : 32;
-  const unsigned down = (unsigned)((p.H + hr - 1) / hr);
-  if (p.T > 16) k_few_down<TY, 2, 2><<<down, kDownWaves * 64, 0, st>>>(p, hr);
-  else if (hr > 16) k_few_down<TY, 2, 1><<<down, kDownWaves * 64, 0, st>>>(p, hr);
-  else k_few_down<TY, 1, 1><<<down, kDownWaves * 64, 0, st>>>(p, hr);
+  const long most = (slots < pairs ? slots : pairs) * (p.F / 16);
+  const DownPlan d = down_plan(p.T, p.H);
+  const auto up = [&](auto epl, auto w) {
+    constexpr int EPL = decltype(epl)::value, W = decltype(w)::value, kMost = 2 * kCus * kRingWaves / W;
+    k_few_up<TY, EPL, W><<<(unsigned)(most < kMost ? most : kMost), W * 64, 0, st>>>(p, d.tiles);
+  };
+  const auto up_w = [&](auto w) {
+    if (p.E <= 128) up(std::integral_constant<int, 2>{}, w);
+    else if (p.E <= 384) up(std::integral_constant<int, 6>{}, w);
+    else up(std::integral_constant<int, 16>{}, w);
+  };
+  // Eight waves a block and one block a compute unit where the items expected (of
+  // slots that uniform routing touches) are no more than the units, else four and two.
+  const double miss = pow(1.0 - (double)p.k / p.E, p.T);
+  if (p.P_local * (1.0 - miss) * (p.F / 16) <= kCus) up_w(std::integral_constant<int, 8>{});
+  else up_w(std::integral_constant<int, 4>{});
+  const unsigned down = (unsigned)(d.tiles * d.zs);
+  if (p.T > 16) k_few_down<TY, 2, 2><<<down, kDownWaves * 64, 0, st>>>(p, d.hr, d.zs);
+  else if (d.hr > 16) k_few_down<TY, 2, 1><<<down, kDownWaves * 64, 0, st>>>(p, d.hr, d.zs);
+  else k_few_down<TY, 1, 1><<<down, kDownWaves * 64, 0, st>>>(p, d.hr, d.zs);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t few_table_bytes() { return sizeof(FewTable); }
+
+// (for any T up to T_max, which has the most rows but not always the most blocks a tile)
+size_t few_sums_bytes(int T_max, int H) {
+  size_t n = 0;
+  for (int T = 1; T <= T_max && T <= kFewMaxT; ++T) {
+    const DownPlan d = down_plan(T, H);
+    const size_t m = d.zs > 1 ? (size_t)d.zs * T * H * sizeof(float) : 0;
+    n = m > n ? m : n;
+  }
+  return n;
+}
 
 hipError_t launch_few(int type, const FewArgs& p, hipStream_t st) {
   return type == kBF16 ? run<kBF16>(p, st) : run<kF16>(p, st);

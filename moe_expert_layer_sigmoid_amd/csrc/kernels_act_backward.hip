@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBack
           if constexpr (G == 2) o[G - 1][e] = v[e] * f;
           far |= g[e] < far_below<ACT>();
         }
-        if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
+        if constexpr (ACT == kActSilu || ACT == kActGelu || ACT == kActGeluTanh) {
           if (far) {  // one branch for all columns: few or no values get there
 #pragma unroll
             for (int e = 0; e < kV; ++e)

@@ -533,11 +533,23 @@ size_t moe_a16w4_workspace_bytes(const moe_dims_t* d) {
   return layout_of(d).total + round_up((size_t)d->T_max * d->k * d->F * 2, kAlign);
 }
 
-size_t moe_a16w16_workspace_bytes(const moe_dims_t* d) {
-  if (check_dims(d) != MOE_OK) return 0;
+namespace {
+// The a16w16 layer's workspace: table, counters, act, sums.
+struct FewLayout {
+  size_t cnt, act, part, total;
+};
+FewLayout few_layout(const moe_dims_t* d) {
   const size_t rows = (size_t)(d->T_max < kFewMaxT ? d->T_max : kFewMaxT) * d->k;
-  return round_up(few_table_bytes(), kAlign) + round_up(rows * d->F * 4, kAlign);
+  FewLayout l;
+  l.cnt = round_up(few_table_bytes(), kAlign);
+  l.act = l.cnt + round_up(kFewTiles * sizeof(int32_t), kAlign);
+  l.part = l.act + round_up(rows * d->F * 4, kAlign);
+  l.total = l.part + round_up(few_sums_bytes(d->T_max, d->H), kAlign);
+  return l;
 }
+}  // namespace
+
+size_t moe_a16w16_workspace_bytes(const moe_dims_t* d) { return check_dims(d) == MOE_OK ? few_layout(d).total : 0; }
 
 int moe_forward_a16w16(const moe_dims_t* d, int32_t type, const int32_t* num_tokens, const void* x, const float* logits,
                        const void* w1, const void* w2, const int32_t* rep_count, const int32_t* rep_slots,
@@ -557,8 +569,9 @@ int moe_forward_a16w16(const moe_dims_t* d, int32_t type, const int32_t* num_tok
   if (d->T == 0) return MOE_OK;
   const moe_taps_t none{};
   const moe_taps_t& tp = taps ? *taps : none;
+  const FewLayout l = few_layout(d);
   const FewArgs p{x, logits, w1, w2, rep_count, rep_slots, num_tokens, load_hist, out, tp.topk_ids, tp.topk_w,
-                  tp.phys_ids, at<void>(ws, round_up(few_table_bytes(), kAlign)), at<FewTable>(ws, 0), d->T, d->H, d->F,
+                  tp.phys_ids, at<void>(ws, l.act), at<FewTable>(ws, 0), at<float>(ws, l.part), at<int32_t>(ws, l.cnt), d->T, d->H, d->F,
                   d->E, d->k, d->P_total, d->p0, d->P_local, d->R_max, d->token_id_base};
   return hip_status(launch_few(type, p, (hipStream_t)stream));
 }

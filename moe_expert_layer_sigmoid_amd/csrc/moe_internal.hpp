@@ -174,7 +174,8 @@ hipError_t launch_gemm2_a16_pairs(const uint16_t* act, int T, int k, const int32
 
 // The layer on 16-bit experts for T <= kFewMaxT tokens (kernels_a16w16.hip), type
 // 0 bf16 or 1 f16: w1 [P_local, 2F, H], w2 [P_local, H, F].  act: 2 T k rows of F
-// values; tab: few_table_bytes().  t_dev, load_hist, ids, wts, phys may be null.
+// values; tab: few_table_bytes(); part: few_sums_bytes(T_max, H); cnt: kFewTiles
+// counters.  t_dev, load_hist, ids, wts, phys may be null.
 constexpr int kFewMaxT = 32;
 struct FewTable;
 struct FewArgs {
@@ -189,10 +190,14 @@ struct FewArgs {
   int32_t* phys;
   void* act;
   FewTable* tab;
+  float* part;
+  int32_t* cnt;
   int T, H, F, E, k, P_total, p0, P_local, R_max;
   uint32_t base;
 };
+constexpr int kFewTiles = 512;  // H / 32 at most
 size_t few_table_bytes();
+size_t few_sums_bytes(int T_max, int H);
 hipError_t launch_few(int type, const FewArgs& p, hipStream_t st);
 
 }  // namespace moe
