@@ -58,7 +58,7 @@ constexpr float kGeluA = 0.044715f;
 // fitted to the scaled complementary error function for the least largest relative
 // error over 0 <= a <= 27 (4.9e-8; with f32's roundings 8 x 2^-24).  One exponential then
 // gives Phi and phi both, and the negative tail keeps its relative error.  (erfcf
-// bound the gradient by its arithmetic: 29343 rows x 672, 46 us for GELU1.)
+// bound the gradient by its arithmetic: 29343 rows x 672, 46 us for 31.)
 __device__ __forceinline__ float scaled_tail(float a) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.27f, a, 1.0f));
   float q = 0.0279833451f;

@@ -23,45 +23,57 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocks = 2048;        // partial sums of all launches together, and one a launch more
 constexpr int kChunkElems = 16384;  // (8192: 1136 us for 1101 at 528 M values in f32)
-constexpr int kTable = 112;          // 3.3 KB of arguments, under the 4 KB limit
+constexpr int kTable = 168;          // with the rest 4072 bytes of arguments, under the 4 KB limit
 
 struct Table {
   const void* in[kTable];
   void* out[kTable];
-  int64_t n[kTable];
-  uint32_t end[kTable];  // chunks up to the tensor's end
-  uint8_t type[kTable];
+  uint32_t end[kTable];   // chunks up to the tensor's end
+  uint32_t last[kTable];  // values of its last chunk, and above 16 bits its type
   int count;
-  int part0;             // the launch's first partial sum
+  int part0;              // the launch's first partial sum
+  uint32_t each, more;    // chunks of a block; the first `more` blocks take one more
 };
+static_assert(sizeof(Table) + 24 <= 4096 && kChunkElems < 1 << 16, "arguments");
 
 typedef v4i v4i_any __attribute__((aligned(2)));
 
 template <int T>
 using Elem = std::conditional_t<T == kBF16, __bf16, std::conditional_t<T == kF16, _Float16, float>>;
 
-// Calls f(tensor, first element, elements) for the block's chunks, in order or
+// A block's run of chunks, and the tensor of its first (back: of its last): found by
+// every wave with three loads at a time and ballots (a binary search in the arguments
+// was seven trips, 1 us of the 4 of a small launch).
+struct Run {
+  uint32_t c0, c1;
+  int i;
+  __device__ __forceinline__ Run(const Table& t, bool back) {
+    const uint32_t b = blockIdx.x;
+    c0 = b * t.each + min(b, t.more);
+    c1 = c0 + t.each + (b < t.more ? 1 : 0);
+    const uint32_t c = back ? c1 - 1 : c0;
+    const int lane = threadIdx.x & 63;
+    i = 0;  // tensors that end at or before c
+#pragma unroll
+    for (int k = 0; k < (kTable + 63) / 64; ++k) {
+      const int j = 64 * k + lane;
+      i += __popcll(__ballot(j < t.count && t.end[min(j, kTable - 1)] <= c));
+    }
+  }
+};
+
+// Calls f(tensor, first element, elements, type) for the run's chunks, in order or
 // backwards.
 template <class F>
-__device__ __forceinline__ void chunks(const Table& t, bool back, F f) {
-  const uint32_t total = t.end[t.count - 1];
-  const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.x / gridDim.x);
-  const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.x + 1) / gridDim.x);
-  if (c0 == c1) return;
-  const uint32_t first = back ? c1 - 1 : c0;
-  int lo = 0, hi = t.count - 1;  // the first tensor whose end is past `first`
-  while (lo < hi) {
-    const int m = (lo + hi) / 2;
-    if (t.end[m] > first) hi = m;
-    else lo = m + 1;
-  }
-  for (uint32_t k = 0; k < c1 - c0; ++k) {
-    const uint32_t c = back ? first - k : first + k;
+__device__ __forceinline__ void chunks(const Table& t, const Run& run, bool back, F f) {
+  int lo = run.i;
+  for (uint32_t k = 0; k < run.c1 - run.c0; ++k) {
+    const uint32_t c = back ? run.c1 - 1 - k : run.c0 + k;
     while (t.end[lo] <= c) ++lo;
     while (lo > 0 && t.end[lo - 1] > c) --lo;
+    const uint32_t last = t.last[lo];
     const int64_t e0 = (int64_t)(c - (lo ? t.end[lo - 1] : 0)) * kChunkElems;
-    const int64_t left = t.n[lo] - e0;
-    f(lo, e0, (int)(left < kChunkElems ? left : kChunkElems));
+    f(lo, e0, c + 1 == t.end[lo] ? (int)(last & 0xFFFF) : kChunkElems, (int)(last >> 16));
   }
 }
 
@@ -74,33 +86,40 @@ template <int T, bool LAST, class F>
 __device__ __forceinline__ void pieces(const Elem<T>* p, int n, F f) {
   constexpr int V = 16 / sizeof(Elem<T>), S = kChunkElems / (V * kThreads);
   v4i x[S];
+  const auto load = [&](int at) {
+    const v4i_any* q = reinterpret_cast<const v4i_any*>(p + at);
+    if constexpr (LAST) return __builtin_nontemporal_load(q);
+    else return (v4i)*q;
+  };
+  const auto use = [&](int s, int at) {
+    Elem<T> v[V];
+    __builtin_memcpy(v, &x[s], 16);
+    f(v, V, at);
+  };
   if (n == kChunkElems) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const v4i_any* q = reinterpret_cast<const v4i_any*>(p + (s * kThreads + threadIdx.x) * V);
-      if constexpr (LAST) x[s] = __builtin_nontemporal_load(q);
-      else x[s] = *q;
-    }
+    for (int s = 0; s < S; ++s) x[s] = load((s * kThreads + threadIdx.x) * V);
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      Elem<T> v[V];
-      __builtin_memcpy(v, &x[s], 16);
-      f(v, V, (s * kThreads + (int)threadIdx.x) * V);
-    }
+    for (int s = 0; s < S; ++s) use(s, (s * kThreads + (int)threadIdx.x) * V);
     return;
   }
-#pragma unroll 1
-  for (int i = threadIdx.x * V; i < n; i += kThreads * V) {
-    Elem<T> v[V];
-    const int m = min(V, n - i);
-    if (m == V) {
-      const v4i w = *reinterpret_cast<const v4i_any*>(p + i);
-      __builtin_memcpy(v, &w, 16);
-    } else {
+  // whole pieces, all of them in flight together; then the values past the last
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = e < m ? p[i + e] : (Elem<T>)0.0f;
-    }
-    f(v, m, i);
+  for (int s = 0; s < S; ++s) {
+    const int at = (s * kThreads + (int)threadIdx.x) * V;
+    if (at + V <= n) x[s] = load(at);
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int at = (s * kThreads + (int)threadIdx.x) * V;
+    if (at + V <= n) use(s, at);
+  }
+  if (n % V && (int)threadIdx.x == n / V % kThreads) {
+    Elem<T> v[V];
+    const int at = n / V * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = at + e < n ? p[at + e] : (Elem<T>)0.0f;
+    f(v, n - at, at);
   }
 }
 
@@ -127,8 +146,8 @@ __device__ __forceinline__ double block_sum(double s) {
 
 __global__ void __launch_bounds__(kThreads) k_grad_squares(Table t, double* part) {
   double s = 0.0;
-  chunks(t, false, [&](int i, int64_t e0, int n) {
-    with_type(t.type[i], [&](auto tc) {
+  chunks(t, Run(t, false), false, [&](int i, int64_t e0, int n, int type) {
+    with_type(type, [&](auto tc) {
       constexpr int T = decltype(tc)::value;
       pieces<T, false>(static_cast<const Elem<T>*>(t.in[i]) + e0, n, [&](const auto& v, int, int) {
 #pragma unroll
@@ -156,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const double* part, int 
 
 __global__ void __launch_bounds__(kThreads) k_grad_scale(Table t, const double* part, int parts, float max_norm,
                                                          float* norm) {
+  const Run run(t, true);  // on its way while the norm is added up
   const double v = norm_of(part, parts);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
   const double q = max_norm / (v + 1e-6);
@@ -163,9 +183,9 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(Table t, const double* 
   // range keeps its bits by a power of two apart
   const float scale = q < 0x1p-64 ? 0x1p-64f : 1.0f;
   const float c = q > 1.0 ? 1.0f : (float)(q / scale);
-  chunks(t, true, [&](int i, int64_t e0, int n) {
+  chunks(t, run, true, [&](int i, int64_t e0, int n, int type) {
     if (c == 1.0f && t.in[i] == t.out[i]) return;  // nothing to change
-    with_type(t.type[i], [&](auto tc) {
+    with_type(type, [&](auto tc) {
       constexpr int T = decltype(tc)::value;
       using E = Elem<T>;
       E* out = static_cast<E*>(t.out[i]) + e0;
@@ -209,15 +229,16 @@ int each_table(const GradTensor* g, int count, F f) {
       total += (uint32_t)chunks_of(g[i]);
       t.in[k] = g[i].in;
       t.out[k] = g[i].out;
-      t.n[k] = g[i].n;
-      t.type[k] = (uint8_t)g[i].type;
       t.end[k] = total;
+      t.last[k] = (uint32_t)((g[i].n - 1) % kChunkElems + 1) | (uint32_t)g[i].type << 16;
     }
     if (!t.count) break;
     // the launch's share of kBlocks blocks, at least one
     const uint64_t share = all <= kBlocks ? total : (uint64_t)total * kBlocks / all;
     const unsigned blocks = (unsigned)(share ? share : 1);
     t.part0 = part;
+    t.each = total / blocks;
+    t.more = total % blocks;
     part += (int)blocks;
     f(t, blocks);
   }

@@ -47,9 +47,9 @@ SIZES = {
     "chunks": [(8191, "bf16"), (8192, "f16"), (8193, "f32"), (16384, "bf16"), (24577, "f32")],
     "empty": [(0, "f32"), (0, "bf16")],
     "large": [(3_000_001, "f32"), (5, "bf16"), (20_000_003, "bf16"), (9_999_999, "f16")],
-    "many": [(1 + 37 * i % 500, ("bf16", "f16", "f32")[i % 3]) for i in range(300)],
-    "table": [(64, "f32")] * 112,
-    "table_and_one": [(64, "f32")] * 113,
+    "many": [(1 + 37 * i % 500, ("bf16", "f16", "f32")[i % 3]) for i in range(500)],
+    "table": [(64, "f32")] * 168,
+    "table_and_one": [(64, "f32")] * 169,
 }
 
 
