@@ -365,6 +365,38 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  // ---- the epilogue's bias and first strip of residual, on their way during the
+  // product where registers allow: as they lie in memory, of the lane's columns if
+  // all of those exist (`finish` reads the others).
+  constexpr bool kEarly = EP != kPlain && TI * TJ <= 16;
+  static_assert(!kEarly || TI <= 4, "early_res holds four rows a lane");
+  constexpr int kOut = EP == kGated ? 2 : 1;  // columns of the product an output column
+  v4i early_bias[kEarly ? kOut : 1], early_res[kEarly ? 4 : 1];
+  if constexpr (kEarly) {
+    const bool wide = pl.out_type == kF32;
+    const int V = wide ? 4 : 8, LR = TI * 16 / kOut / V, n_out = p.N / kOut;
+    const int co = c0 / kOut + wa * (TI * 16 / kOut) + lane % LR * V;
+    if (pl.splits == 1 && co + V <= n_out) {
+      if (p.bias) {
+#pragma unroll
+        for (int h = 0; h < kOut; ++h) {
+          const char* b = static_cast<const char*>(p.bias) + ((size_t)g * p.N + h * n_out + co) * 2;
+          typedef v2i v2i_any __attribute__((aligned(2)));
+          const v2i lo = *reinterpret_cast<const v2i_any*>(b), hi = wide ? v2i{0, 0} : *reinterpret_cast<const v2i_any*>(b + 8);
+          early_bias[h] = v4i{lo.x, lo.y, hi.x, hi.y};
+        }
+      }
+      if (p.res) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = wb * TJ * 16 + k * (64 / LR) + lane / LR;
+          if (k * (64 / LR) < 16 && r < nr)
+            early_res[k] = load16(static_cast<const char*>(p.res) + ((row0 + r) * n_out + co) * (wide ? 4 : 2));
+        }
+      }
+    }
+  }
+
   // ---- main loop.  A stage is U steps of one A tile against all of the wave's
   // B tiles (fp8: whole 128 columns; 16-bit: half by half).  A's operands are
   // read D steps ahead, and the last D steps of a stage run after the barrier
@@ -600,17 +632,27 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
     const int nc = min(V, n_out - co);                                          // that exist (may be negative)
     float bias[G][V];
 #pragma unroll
-    for (int h = 0; h < G; ++h)
+    for (int h = 0; h < G; ++h) {
+      if (kEarly && nc == V) {
+        B x[8];
+        __builtin_memcpy(x, &early_bias[kEarly ? h : 0], 16);
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        bias[h][e] = p.bias && e < nc ? (float)static_cast<const B*>(p.bias)[(size_t)g * p.N + h * n_out + co + e] : 0.0f;
+        for (int e = 0; e < V; ++e) bias[h][e] = p.bias ? (float)x[e] : 0.0f;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          bias[h][e] = p.bias && e < nc ? (float)static_cast<const B*>(p.bias)[(size_t)g * p.N + h * n_out + co + e] : 0.0f;
+      }
+    }
     O res[2][KI][V];
     auto fetch = [&](int j) {
 #pragma unroll
       for (int k = 0; k < KI; ++k) {
         const int r = wb * TJ * 16 + 16 * j + k * RI + lane / LR;
         const O* s = static_cast<const O*>(p.res) + (row0 + r) * n_out + co;
-        if (r < nr && nc == V) {
+        if (kEarly && j == 0 && nc == V) {
+          __builtin_memcpy(res[0][k], &early_res[kEarly ? k : 0], 16);
+        } else if (r < nr && nc == V) {
           const v4i w = load16(s);
           __builtin_memcpy(res[j % 2][k], &w, 16);
         } else {

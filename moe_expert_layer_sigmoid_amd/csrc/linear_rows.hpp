@@ -113,16 +113,24 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
 #pragma unroll
     for (int a = 0; a < G; ++a) g.acc[a][0] = v4f{0.f, 0.f, 0.f, 0.f};
   };
+  // what the epilogue adds, on its way during the product: as it lies in memory, so
+  // that nothing waits for it before `finish`
+  uint32_t bias[G] = {}, res = 0;
+  const auto ahead = [&](const Part& x) {
+    const int j = tid / 16, col = x.c0 + tid % 16;
+    if (j >= x.nr || tid % 16 >= x.n) return;
+    const size_t o = (size_t)(x.r0 + j) * n_out + col;
+    if (p.bias) {
+#pragma unroll
+      for (int h = 0; h < G; ++h) bias[h] = static_cast<const uint16_t*>(p.bias)[(size_t)x.g * p.N + h * n_out + col];
+    }
+    if (p.res) res = out_type == kF32 ? static_cast<const uint32_t*>(p.res)[o] : static_cast<const uint16_t*>(p.res)[o];
+  };
   const auto finish = [&](const Part& x) {
     const int j = tid / 16, col = x.c0 + tid % 16;
     const bool here = j < x.nr && tid % 16 < x.n;  // (nr <= 16: the first four waves)
     const size_t row = (size_t)(x.r0 + j), o = row * n_out + col;
-    float bias[G] = {}, res = 0.0f;
-    if (p.bias && here) {
-#pragma unroll
-      for (int h = 0; h < G; ++h) bias[h] = (float)static_cast<const B*>(p.bias)[(size_t)x.g * p.N + h * n_out + col];
-    }
-    if (p.res && here) res = out_type == kF32 ? static_cast<const float*>(p.res)[o] : (float)static_cast<const B*>(p.res)[o];
+    const auto value = [](uint32_t w) { return (float)__builtin_bit_cast(B, (uint16_t)w); };
     v4f v[G];
     float z[G], y = 0.0f;
 #pragma unroll
@@ -135,11 +143,11 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
     if (here) {
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        z[h] += bias[h];
+        z[h] += value(bias[h]);
         if (p.pre) put(p.pre, row * p.N + h * n_out + col, z[h]);
       }
       with_act(p.act, [&](auto a) { y = act_mul<decltype(a)::value>(z[0], G == 2 ? z[G - 1] : 1.0f); });
-      put(p.out, o, y + res);
+      put(p.out, o, y + (out_type == kF32 ? __uint_as_float(res) : value(res)));
     }
   };
   if (const int per = (kst + W - 1) / W; per <= R::PRE) {  // short: one burst a part
@@ -148,6 +156,7 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
       clear();
       next = at;
       seek();
+      ahead(x);
       burst<R>(mine, per, issue, g);
       finish(x);
       at += x.n;
@@ -155,14 +164,17 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
     return;
   }
   seek();
+  Part x = part(at);
+  ahead(x);
   for (int n = -1;; ++n) {
     if (n <= 0) clear();
     stages(mine, mine, n < 0);
     if (n + 1 < rounds) continue;
-    const Part x = part(at);
     finish(x);
     at += x.n;
     if (at >= end) break;
+    x = part(at);
+    ahead(x);
     n = -1;  // the next columns' first stages are on their way
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
