@@ -33,7 +33,7 @@ constexpr int kPairs = kFewMaxT * 16;  // T k at most
 // The touched slots, ascending; the pairs of an entry are act rows [start, start +
 // popc(mask)), one per bit (token) of mask, ascending.  A slot with more than 16 tokens
 // is two entries (its weights are then read twice, the second time mostly from
-// a cache; a second tile of tokens for every slot cost the others 6 %).
+// a cache).
 struct FewTable {
   int n;
   int pad[3];
@@ -248,7 +248,10 @@ __global__ void __launch_bounds__(W * 64, 2) k_few_up(FewArgs p, int ncnt) {
     const int j = tid / 16;  // (np <= 16: the first four waves)
     if (j < np) {
       using T = Half<TY>;
-      const float a = act_mul<kActSilu>(s[0], s[1]) * r.w[start + j];
+      const float gate[1] = {s[0]}, up[1] = {s[1]};
+      float y[1];
+      act_row<kActSilu>(gate, up, y);
+      const float a = y[0] * r.w[start + j];
       const T hi = (T)a;
       const float rest = a - (float)hi;
       T* const o = static_cast<T*>(p.act) + (size_t)(start + j) * F + ct * 16 + tid % 16;

@@ -701,10 +701,7 @@ __global__ void __launch_bounds__(C::KS * C::W * 64, C::OCC * C::KS * C::W / 4) 
 #pragma unroll
           for (int h = 0; h < G; ++h) put(o + h * n_out, z[h]);
         }
-        with_act(p.act, [&](auto a) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = act_mul<decltype(a)::value>(z[0][e], G == 2 ? z[G - 1][e] : 1.0f);
-        });
+        with_act(p.act, [&](auto a) { act_gated<decltype(a)::value>(z, v); });
         if (p.res) {
 #pragma unroll
           for (int e = 0; e < V; ++e) v[e] += (float)res[j % 2][k][e];
@@ -945,10 +942,7 @@ __global__ void __launch_bounds__(256) k_linear_join_act(LinearArgs p, int split
       for (int e = 0; e < 4; ++e) z[h][e] += bias[h][e];
       if (p.pre && in) put(static_cast<O*>(p.pre) + (size_t)row * p.N + h * n_out + c, z[h]);
     }
-    with_act(p.act, [&](auto a) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_mul<decltype(a)::value>(z[0][e], G == 2 ? z[G - 1][e] : 1.0f);
-    });
+    with_act(p.act, [&](auto a) { act_gated<decltype(a)::value>(z, v); });
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += res[e];
     if (in) put(static_cast<O*>(p.out) + (size_t)row * n_out + c, v);

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
     const size_t row = (size_t)(x.r0 + j), o = row * n_out + col;
     const auto value = [](uint32_t w) { return (float)__builtin_bit_cast(B, (uint16_t)w); };
     v4f v[G];
-    float z[G], y = 0.0f;
+    float z[G], y[1];
 #pragma unroll
     for (int a = 0; a < G; ++a) v[a] = g.acc[a][0];
     reduce<G, W>(red, v, z);
@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
         z[h] += value(bias[h]);
         if (p.pre) put(p.pre, row * p.N + h * n_out + col, z[h]);
       }
-      with_act(p.act, [&](auto a) { y = act_mul<decltype(a)::value>(z[0], G == 2 ? z[G - 1] : 1.0f); });
-      put(p.out, o, y + (out_type == kF32 ? __uint_as_float(res) : value(res)));
+      const float gate[1] = {z[0]}, up[1] = {G == 2 ? z[G - 1] : 1.0f};
+      with_act(p.act, [&](auto a) { act_row<decltype(a)::value>(gate, up, y); });
+      put(p.out, o, y[0] + (out_type == kF32 ? __uint_as_float(res) : value(res)));
     }
   };
   if (const int per = (kst + W - 1) / W; per <= R::PRE) {  // short: one burst a part

@@ -55,8 +55,8 @@ __device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT, P>& g
 }
 
 // All of a wave's `per` <= PRE stages in one burst: short reductions, where a full
-// ring would wait for stages that are not there (the tiny layer: 5.8 + 7.5 us for
-// TINY0 + TINY1).
+// ring would wait for stages that are not there (two tokens, H 128, F 32, 8 experts:
+// 5.5 + 3.4 us in one burst, 6.4 + 8.3 through the ring).
 template <class R, class Issue>
 __device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, R& g) {
 #pragma unroll
