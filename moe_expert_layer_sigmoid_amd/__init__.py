@@ -822,8 +822,8 @@ class GradList:
     that their addresses stay theirs; make a new one when gradients move."""
 
     def __init__(self, grads, outs=None):
-        self.grads = list(grads)
-        self.outs = self.grads if outs is None else list(outs)
+        self.grads = tuple(grads)
+        self.outs = self.grads if outs is None else tuple(outs)
         if len(self.outs) != len(self.grads):
             raise ValueError(f"outs: {len(self.outs)} tensors for {len(self.grads)}")
         self.device = -1

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(W * 64, 2) k_few_up(FewArgs p, int ncnt) {
     for (; item < items; item += gridDim.x) {
       clear();
       seek();
-      burst<R>(mine, per, issue, g);
+      burst<R>(mine, per, issue, [&](const lds_u8* from, int u) { consume(from, g, u); });
       finish(item);
     }
     return;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
   int at = first + wave;          // the next loads: stage of all,
   int i = at / kst, s = at % kst;  // entry, stage of it
   rsrc_t wr = none;
-  uint32_t bvo[NT];
+  uint32_t bvo[NT], on = 0, held = 0;  // on: bit c: entry i has the lane's token of tile c; held: of each stage in the ring
   auto seek = [&]() {  // of entry i
     const bool live = i < nt;
     const int ii = live ? i : 0;
@@ -337,9 +337,11 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
     const uint32_t mask = live ? tab.mask[ii] : 0;
     const int start = live ? tab.start[ii] : 0;
     wr = make_rsrc(static_cast<const uint8_t*>(p.w2) + ((size_t)slot * H + h0) * rowb, live ? (uint32_t)nh * rowb : 0u);
+    on = 0;
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
       const int t = 16 * c + l16;
+      on |= (mask >> t & 1) << c;
       bvo[c] = mask >> t & 1 ? (uint32_t)(start + __popc(mask & ((1u << t) - 1))) * rowb + 16u * q : kOob;
     }
   };
@@ -364,12 +366,29 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
           g.b[u][2 * c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
           g.b[u][2 * c + 1][kk] = buf_load16(b, bvo[c] + half, so + 64u * kk);  // (kOob + half: still past every buffer)
         }
+      held = (held & ~(((1u << NT) - 1) << (u * NT))) | on << (u * NT);
       at += W;
       if ((s += W) >= kst) {
         i += s / kst;
         s %= kst;
         seek();
       }
+    };
+    // A stage's products; the sums of the tokens that its expert does not see stay as they
+    // were (zeros times a weight that is not finite would be NaN).
+    auto eat = [&](const lds_u8* from, int u) __attribute__((always_inline)) {
+      v4f old[NA][NT];
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) old[a][c] = g.acc[a][c];
+      consume(from, g, u);
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g.acc[a][c][e] = held >> (u * NT + c) & 1 ? g.acc[a][c][e] : old[a][c][e];
     };
     auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
       if (first) {
@@ -382,13 +401,13 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((R::PRE - 1) * R::I) : "memory");
         __builtin_amdgcn_sched_barrier(0);
         issue(to, (u + R::PRE) % R::NS);
-        consume(from + u * R::kSlot, g, u);
+        eat(from + u * R::kSlot, u);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     lds_u8* const mine = (lds_u8*)ring + wave * kRingBytes;
     if (const int per = (each + W - 1) / W; per <= R::PRE) {
-      burst<R>(mine, per, issue, g);
+      burst<R>(mine, per, issue, eat);
     } else {
       for (int n = -1; n < rounds; ++n) stages(mine, mine, n < 0);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block

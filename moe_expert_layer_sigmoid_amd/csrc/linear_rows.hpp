@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(W * 64, 2) k_linear_rows(LinearArgs p, int out
       next = at;
       seek();
       ahead(x);
-      burst<R>(mine, per, issue, g);
+      burst<R>(mine, per, issue, [&](const lds_u8* from, int u) { consume(from, g, u); });
       finish(x);
       at += x.n;
     }

@@ -57,8 +57,8 @@ __device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT, P>& g
 // All of a wave's `per` <= PRE stages in one burst: short reductions, where a full
 // ring would wait for stages that are not there (two tokens, H 128, F 32, 8 experts:
 // 5.5 + 3.4 us in one burst, 6.4 + 8.3 through the ring).
-template <class R, class Issue>
-__device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, R& g) {
+template <class R, class Issue, class Eat>
+__device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, Eat eat) {
 #pragma unroll
   for (int u = 0; u < R::PRE; ++u)
     if (u < per) issue(mine, u);
@@ -66,7 +66,7 @@ __device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, R& g) 
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int u = 0; u < R::PRE; ++u)
-    if (u < per) consume(mine + u * R::kSlot, g, u);
+    if (u < per) eat(mine + u * R::kSlot, u);
 }
 
 // The W waves' sums of acc[a][c], by thread of the first four waves (token column

@@ -223,3 +223,22 @@ def test_far_gates_and_f16_overflow():
     c.w2.fill_(1.0)
     c.run()
     assert torch.all(torch.isinf(c.out))
+
+
+@pytest.mark.parametrize("n,H,F", [(3, 128, 128), (3, 2176, 256), (20, 256, 512), (20, 2176, 2048), (16, 8320, 1024)])
+def test_weights_of_an_expert_that_are_not_finite_stay_with_its_tokens(n, H, F):
+    """A token's output is a sum over its own experts; 0 times another's infinity has no place in it."""
+    c = Case(n, H, F, 6, 2, seed=9)
+    c.run()
+    ids = c.taps["topk_ids"].view(n, 2)
+    bad = int(ids[0, 0])
+    slot = int(c.rs[bad, 0])
+    clean = c.out.clone()
+    c.w2[slot, ::3] = float("inf")
+    c.w2[slot, 1::3] = float("nan")
+    c.run()
+    torch.cuda.synchronize()
+    hit = (ids == bad).any(dim=1)
+    assert hit.any() and not hit.all()
+    assert torch.equal(c.out[~hit], clean[~hit])
+    assert not torch.isfinite(c.out[hit][:, 0]).any() and torch.isnan(c.out[hit][:, 1::3]).all()
