@@ -13,7 +13,8 @@
 // error as the output's own rounding (normwise 0.0024 for 0.0017 in bf16), and the
 // matrix instructions have time to spare.
 // MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
-// experts' weights, streamed as ring.hpp says.
+// experts' weights, streamed as ring.hpp says: H 7168, F 2048, bf16, one token on 6
+// experts 57 + 31 us (6.2 and 5.8 TB/s), 16 tokens on 42 375 + 183 (6.7 and 6.9).
 
 #include <hip/hip_runtime.h>
 

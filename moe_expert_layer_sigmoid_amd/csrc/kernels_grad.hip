@@ -8,7 +8,8 @@
 // that the result can show, whatever the order, and the order is fixed.  Every
 // block of the scaling launch adds the partial sums (a few KB, from L2) itself
 // and walks its run backwards, so that what the first pass read last is read first.
-// Bound by memory.
+// Bound by memory: 528 M values in f32 342 us (6.2 TB/s) and 749 (5.6 TB/s, reads and
+// writes; a copy reaches 5.2).
 
 #include <hip/hip_runtime.h>
 
@@ -42,8 +43,8 @@ template <int T>
 using Elem = std::conditional_t<T == kBF16, __bf16, std::conditional_t<T == kF16, _Float16, float>>;
 
 // A block's run of chunks, and the tensor of its first (back: of its last): found by
-// every wave with three loads at a time and ballots (a binary search in the arguments
-// was seven trips, 1 us of the 4 of a small launch).
+// every wave with three loads at a time and ballots (36 tensors: 4.2 and 5.2 us a
+// launch; by a binary search in the arguments, seven trips, 4.6 and 5.7).
 struct Run {
   uint32_t c0, c1;
   int i;

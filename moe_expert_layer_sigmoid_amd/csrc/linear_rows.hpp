@@ -3,9 +3,9 @@
 // is joined in memory.  A block takes an equal share of the groups' output columns, 16
 // at a time (gated: 16 gate and 16 up columns); W waves a block: eight, one block a
 // compute unit, where that gives a unit 16 columns at most, else four and two.  Bound by the weights and by
-// the latency of one burst.  (One row, 4096 x 7168, gated: 13.7 us, 18.0 by a block's
-// eight waves loading weights into registers; 512 x 7168 plain 8.7 and 11.0; 1024 x
-// 1024 gated 6.3, by tiles 7.6.  More rows a group read x too often for that: 48 rows,
+// the latency of one burst.  (One row, 4096 x 7168, gated: 13.1 us, 18.0 by a block's
+// eight waves loading weights into registers; 512 x 7168 plain 8.5 and 11.0; 1024 x
+// 1024 gated 4.2, by tiles 7.6.  More rows a group read x too often for that: 48 rows,
 // 4096 x 7168 gated, took 25.6 against 17.8 by tiles.)
 #pragma once
 
