@@ -495,7 +495,8 @@ int moe_grouped_linear_act(const moe_linear_t* d, int32_t act, int32_t gated, co
  * [groups, N], overwritten, added up from the f32 values before their rounding.
  * (The residual's gradient is dy.)  relu'(0) = 0.  N a multiple of 8; K is not
  * used but must be valid.  dz may be pre itself where the types are the same.
- * The workspace is needed for db alone.  One launch, or two for db. */
+ * The workspace is needed for db alone.  One launch; for db of more rows than
+ * a few blocks can add up (256 at most), two. */
 int moe_grouped_linear_act_backward(const moe_linear_t* d, int32_t act, int32_t gated, const void* dy, const void* pre,
                                     const int32_t* offsets, void* dz, float* db, void* workspace,
                                     size_t workspace_bytes, moe_stream_t stream);

@@ -3,13 +3,14 @@
 //   dz = dy act'(z),  or with z = (gate, up):  dz = (dy up act'(gate), dy act(gate)),
 //   db_g = sum over the group's rows of dz (f32, before dz is rounded).
 // One pass, bound by memory: 49152 rows of 48 groups, 4096 columns gated, 213 us for
-// 1.0 GB (4.7 TB/s; a copy reaches 5.2) and 8 for the sums.  A block takes a tile of rows of one group and all
-// columns that 256 threads hold, eight a thread, so that a column's sum stays in
-// registers and crosses threads once, through LDS.  The tiles are as long as it
-// takes for the card to hold all of them at a time: no second round of blocks that
-// leaves most of it idle.  A tile's sums are f32 partial sums in the workspace, added in
-// row order by a second launch; up to kWhole rows in all a group is one block,
-// which writes db itself.
+// 1.0 GB (4.7 TB/s; a copy reaches 5.2) and 8 for the sums.  A block takes a tile of
+// rows of one group and all columns that 256 threads hold, eight a thread, so that a
+// column's sum stays in registers and crosses threads once, through LDS.  The tiles are
+// as long as it takes for the card to hold all of them at a time: no second round of
+// blocks that leaves most of it idle.  A tile's sums are f32 partial sums in the
+// workspace, added in row order by a second launch.  Up to 256 rows in all, a block
+// takes all rows of a group and few columns, and writes db itself (250 rows of 9 groups,
+// 264 columns: 6.9 us, in two launches 9.6).
 
 #include <hip/hip_runtime.h>
 
@@ -21,8 +22,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kV = 8;        // columns a thread
-constexpr int kWhole = 64;   // rows up to which a group is one block
+constexpr int kV = 8;           // columns a thread
+constexpr int kWhole = 256;     // rows up to which a group's columns may be one block's
+constexpr int kWholeRows = 8;   // ... and of a thread, one after the other
+constexpr int kFewRows = 4;     // rows of a thread up to which it has two in flight
 // blocks that a compute unit's registers hold (gated: three operands in flight and twice the sums)
 constexpr int resident(int ep) { return ep == kGated ? 3 : 4; }
 
@@ -104,11 +107,10 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int groups, int ro
 
 // per: threads across the columns of a block; ncb blocks across; len: rows of a
 // tile, 0 for a group a block.  sums: the partial sums [tile][N], or db itself (len 0).
-template <int IN, int PT, int EP, int ACT>
+template <int IN, int PT, int EP, int ACT, int kAhead>
 __global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBackwardArgs p, int per, int ncb, int len, bool once, float* sums) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int G = EP == kGated ? 2 : 1;
-  constexpr int kAhead = PT == kF32 ? 2 : 4;  // rows a thread has in flight
   __shared__ float red[kThreads][G * kV + 1];
   const int n_out = p.N / G;
   const int tile = blockIdx.x / ncb, cb = blockIdx.x % ncb;
@@ -180,22 +182,26 @@ __global__ void __launch_bounds__(kThreads, resident(EP)) k_act_backward(ActBack
     const int w = i / (G * kV), k = i % (G * kV), col = (cb * per + w) * kV + k % kV;
     if (col >= n_out) continue;
     float s = red[w][k];
+#pragma unroll 8
     for (int t = 1; t < subs; ++t) s += red[w + t * per][k];
     sums[(size_t)tile * p.N + k / kV * n_out + col] = s;
   }
 #endif
 }
 
-// db[g] = the group's partial sums in order: 64 columns a block, four a thread, the
-// tiles dealt to 16 threads a column in runs.  tiles: that the workspace holds
-// (offsets that fall, against the contract, would count more).
-__global__ void __launch_bounds__(256) k_act_backward_join(const float* part, const int32_t* off, int rows, int N, int len,
-                                                           int tiles, float* db) {
+// db[g] = the group's partial sums, the tiles dealt to the threads of a column in
+// runs, the runs' sums added in pairs.  across: threads (of four columns) across a
+// block: 16, or 4 where so few columns leave most of the card idle (38808 rows of
+// 216: both launches 22.2 us, with 16 24.0).  tiles: that the workspace holds (offsets that fall, against the
+// contract, would count more).
+__global__ void __launch_bounds__(kThreads) k_act_backward_join(const float* part, const int32_t* off, int rows, int N, int len,
+                                                                int tiles, int across, float* db) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ v4f red[16][16];
-  const int g = blockIdx.y, lane = threadIdx.x & 63, col = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int c = blockIdx.x * 64 + col * 4;  // N % 8 == 0
-  int before = 0, lo, hi;                   // tiles of the groups before
+  __shared__ v4f red[kThreads / 64][16];
+  const int g = blockIdx.y, lane = threadIdx.x & 63, slices = kThreads / across;
+  const int col = threadIdx.x % across, slice = threadIdx.x / across;
+  const int c = (blockIdx.x * across + col) * 4;  // N % 8 == 0
+  int before = 0, lo, hi;                         // tiles of the groups before
   for (int k = lane; k < g; k += 64) {
     group_rows(off, k, rows, lo, hi);
     before += (hi - lo + len - 1) / len;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(256) k_act_backward_join(const float* part, co
 #pragma unroll
   for (int d = 32; d; d /= 2) before += __shfl_xor(before, d);
   group_rows(off, g, rows, lo, hi);
-  const int n = min((hi - lo + len - 1) / len, max(0, tiles - before)), each = (n + 15) / 16;
+  const int n = min((hi - lo + len - 1) / len, max(0, tiles - before)), each = (n + slices - 1) / slices;
   const int t0 = min(n, slice * each), t1 = min(n, t0 + each);
   v4f s = {0.f, 0.f, 0.f, 0.f};
   if (c < N) {
@@ -217,11 +223,14 @@ __global__ void __launch_bounds__(256) k_act_backward_join(const float* part, co
         if (t + k < t1) s += x[k];
     }
   }
-  red[slice][col] = s;
+  for (int d = across; d < 64; d *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += __shfl_xor(s[e], d);
+  if (lane < across) red[threadIdx.x / 64][lane] = s;
   __syncthreads();
   if (slice == 0 && c < N) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s += red[k][col];
+    for (int w = 1; w < kThreads / 64; ++w) s += red[w][col];
     *reinterpret_cast<v4f*>(db + (size_t)g * N + c) = s;
   }
 #endif
@@ -245,20 +254,48 @@ Division divide(int rows, int n_out, int groups, int ep) {
   return d;
 }
 
+// Threads across a block that takes all rows of a group: 8 (128 bytes of a row), fewer
+// where a thread would have more than kWholeRows / 4 rows should one group hold
+// them all, more where the blocks would be too many; 0 if kWholeRows are then not enough.
+// What a thread has to compute counts here, with one wave a SIMD: gelu_tanh, 64 rows of
+// 4096 columns, gated, 6.0 us, 69 by 256 threads across; 512 rows of 256 columns with 16
+// rows a thread 20, with 4 9.3, in two launches 9.0.
+int whole_across(int rows, int n_out, int groups) {
+  const int chunks = ceil_div(n_out, kV);
+  int per = 8;
+  while (per > 2 && rows * per > kWholeRows / 4 * kThreads) per /= 2;
+  while (per < kThreads && (long)groups * ceil_div(chunks, per) > 4 * kCus * resident(kAct)) per *= 2;
+  if (per > chunks) per = chunks;
+  return rows <= kWhole && rows * per <= kWholeRows * kThreads ? per : 0;
+}
+
 template <int IN, int PT, int EP>
 hipError_t run(const ActBackwardArgs& p, void* ws, hipStream_t st) {
-  const Division d = divide(p.rows, p.N / (EP == kGated ? 2 : 1), p.groups, EP);
-  const bool whole = p.db && p.rows <= kWhole;
+  const int n_out = p.N / (EP == kGated ? 2 : 1), across = p.db ? whole_across(p.rows, n_out, p.groups) : 0;
+  const bool whole = across > 0;
+  Division d = divide(p.rows, n_out, p.groups, EP);
+  if (whole) {
+    d.per = across;
+    d.ncb = ceil_div(ceil_div(n_out, kV), across);
+  }
   float* sums = whole ? p.db : p.db ? static_cast<float*>(ws) : nullptr;
   const unsigned blocks = (unsigned)((whole ? p.groups : d.tiles) * d.ncb);
   // what passes the caches moves with the streaming policy
   const bool once = (size_t)p.rows * p.N * 4 > kStreamMin;
+  // (few rows a thread: the code of four side by side takes longer to load than it saves;
+  // 256 rows of 48 groups, 4096 columns 9.4 us for 11.0)
+  const bool few = whole || d.len * d.per <= kFewRows * kThreads;
   const auto launch = [&](auto a) {
-    k_act_backward<IN, PT, EP, decltype(a)::value><<<blocks, kThreads, 0, st>>>(p, d.per, d.ncb, whole ? 0 : d.len, once, sums);
+    constexpr int ACT = decltype(a)::value, kMost = PT == kF32 ? 2 : 4;
+    if (few) k_act_backward<IN, PT, EP, ACT, 2><<<blocks, kThreads, 0, st>>>(p, d.per, d.ncb, whole ? 0 : d.len, once, sums);
+    else k_act_backward<IN, PT, EP, ACT, kMost><<<blocks, kThreads, 0, st>>>(p, d.per, d.ncb, d.len, once, sums);
   };
   with_act(p.act, launch);
-  if (p.db && !whole)
-    k_act_backward_join<<<dim3((unsigned)ceil_div(p.N, 64), p.groups), 256, 0, st>>>(sums, p.off, p.rows, p.N, d.len, d.tiles, p.db);
+  if (p.db && !whole) {
+    const int wide = (long)ceil_div(p.N, 64) * p.groups < kCus ? 4 : 16;
+    k_act_backward_join<<<dim3((unsigned)ceil_div(p.N, 4 * wide), p.groups), kThreads, 0, st>>>(sums, p.off, p.rows, p.N, d.len,
+                                                                                                d.tiles, wide, p.db);
+  }
   return hipGetLastError();
 }
 
@@ -277,8 +314,9 @@ hipError_t launch_act_backward(int in_type, int out_type, bool gated, const ActB
 
 // (gated or not)
 size_t act_backward_workspace(int rows, int N, int groups) {
-  if (rows <= kWhole) return 0;
-  const int a = divide(rows, N, groups, kAct).tiles, b = divide(rows, N / 2 > 0 ? N / 2 : 1, groups, kGated).tiles;
+  const int half = N / 2 > 0 ? N / 2 : 1;
+  if (whole_across(rows, N, groups) && whole_across(rows, half, groups)) return 0;
+  const int a = divide(rows, N, groups, kAct).tiles, b = divide(rows, half, groups, kGated).tiles;
   return (size_t)(a > b ? a : b) * N * sizeof(float);
 }
 

@@ -270,6 +270,18 @@ def test_backward(rows, groups, N, act, gated):
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,groups,N", [(256, 1, 264), (257, 1, 264), (256, 1, 16), (256, 40, 4104), (64, 96, 4104), (128, 96, 4104), (129, 96, 4104),
+                                           (16, 1024, 2056), (17, 1024, 2056), (250, 7, 4096), (256, 3, 72)])
+def test_backward_in_one_launch_and_in_two(rows, groups, N, gated):
+    """On both sides of the sizes up to which a block takes all rows of a group, all rows in one group too."""
+    _say(f"[case] backward rows={rows} groups={groups} N={N} gated={gated}")
+    Back(rows, groups, N, "silu", gated).check()
+    if groups > 1:
+        off = np.where(np.arange(groups + 1) > groups // 2, rows, 0).astype(np.int32)
+        Back(rows, groups, N, "gelu", gated, out="f32", off=off).check()
+
+
+@pytest.mark.parametrize("gated", [False, True])
 def test_backward_of_many_rows(gated):
     Back(20000, 1, 136, "silu", gated, out="f32").check()
     Back(20000, 3, 2064, "gelu", gated).check()
