@@ -44,7 +44,6 @@ struct FewTable {
 
 namespace {
 
-
 // ---- routing: the block's view of all tokens -------------------------------
 struct Routed {
   FewTable tab;
