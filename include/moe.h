@@ -538,9 +538,9 @@ int moe_grad_clip(const moe_tensor_t* tensors, int32_t count, float max_norm, fl
  * e its slot,  h = w1_e x_t,  act = silu(h[:F]) * h[F:],  out_t = sum over j of
  * topk_w[t][j] w2_e act.  x and out [T, H], w1 [P_local, 2F, H] and w2 [P_local,
  * H, F] of `type` (BF16 or F16), in their natural layout, as moe_grouped_linear
- * takes them.  Sums, activation and weights are f32; topk_w * act enters the
- * second product as two numbers of `type` (to twice its bits; F16: finite up to
- * 65504), and out is rounded once.
+ * takes them.  Sums, activation, weights and topk_w * act are f32 (F16: of 64
+ * columns in a row, the second product takes what is above 2^-38 of the largest),
+ * and out is rounded once.
  * Tokens with no local pair get +0.  T <= 32, else MOE_ERR_UNSUPPORTED (more
  * tokens: moe_quant_permute's buckets with moe_grouped_linear_act).
  * num_tokens (nullable, DEVICE i32, 4-byte aligned): the step's token count n,

@@ -8,10 +8,12 @@
 //               rows of H for all tokens and all slots, so that sums stay in
 //               f32 accumulators from the first slot to the last and nothing is
 //               joined in memory.
-// act goes from one to the other as two numbers of the operands' type whose sum is
-// the f32 value to twice the type's bits: rounded once, it would bring as much
-// error as the output's own rounding (normwise 0.0024 for 0.0017 in bf16), and the
-// matrix instructions have time to spare.
+// act goes from one to the other in f32, and the second product takes it in three
+// parts of the operands' type that add up to it, so that no bit and no range of it
+// is lost (rounded once to 16 bits, it would bring as much error as the output's own
+// rounding: normwise 0.0024 for 0.0017 in bf16; in two 16-bit parts, f16's range ended
+// at 65504.  Parted in each block as it is used: both launches for 32 tokens on 48 of
+// 384 experts 312 us, f16 323, for 303 with two parts stored).
 // MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
 // experts' weights, streamed as ring.hpp says: H 7168, F 2048, bf16, one token on 6
 // experts 57 + 31 us (6.2 and 5.8 TB/s), 16 tokens on 42 375 + 183 (6.7 and 6.9).
@@ -247,16 +249,10 @@ __global__ void __launch_bounds__(W * 64, 2) k_few_up(FewArgs p, int ncnt) {
     reduce<2, W>(red, v, s);
     const int j = tid / 16;  // (np <= 16: the first four waves)
     if (j < np) {
-      using T = Half<TY>;
       const float gate[1] = {s[0]}, up[1] = {s[1]};
       float y[1];
       act_row<kActSilu>(gate, up, y);
-      const float a = y[0] * r.w[start + j];
-      const T hi = (T)a;
-      const float rest = a - (float)hi;
-      T* const o = static_cast<T*>(p.act) + (size_t)(start + j) * F + ct * 16 + tid % 16;
-      o[0] = hi;
-      o[(size_t)p.T * p.k * F] = (T)(fabsf((float)hi) == INFINITY ? 0.0f : rest);  // (f16 past its range: infinite)
+      p.act[(size_t)(start + j) * F + ct * 16 + tid % 16] = y[0] * r.w[start + j];
     }
   };
   if (const int per = (kst + kWaves - 1) / kWaves; per <= R::PRE) {  // short: one burst an item
@@ -281,6 +277,44 @@ __global__ void __launch_bounds__(W * 64, 2) k_few_up(FewArgs p, int ncnt) {
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the block
 #endif
+}
+
+// ---- f32 operands of 16-bit matrix instructions -----------------------------
+// The largest of a value over the four lanes l16 + 16 q, in each of them.
+__device__ __forceinline__ float max_of_quads(float m) {
+  const uint32_t a = __float_as_uint(m);
+  const auto x = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+
+// Eight finite values (or NaN) as parts[0] + parts[1] + parts[2], each truncated to
+// its bits: 24 bits are 8 + 8 + 8 of bf16, 11 + 11 + 2 of f16.  Parts of f16 end at 2^-24.
+template <int TY>
+__device__ __forceinline__ void split(const float (&v)[8], v4i (&parts)[3]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float a = v[e], b = v[e + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if constexpr (TY == kBF16) {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        parts[k][e / 2] = (int)__builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        if (k < 2) {
+          a -= __uint_as_float(ua & 0xFFFF0000u);
+          b -= __uint_as_float(ub & 0xFFFF0000u);
+        }
+      } else {
+        const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
+        parts[k][e / 2] = __builtin_bit_cast(int, h);
+        if (k < 2) {
+          a -= (float)h[0];
+          b -= (float)h[1];
+        }
+      }
+    }
+  }
 }
 
 // hr <= 16 NA: rows of H a block.  Few rows of H leave compute units idle: zs blocks
@@ -317,14 +351,12 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
   const int h0 = tile * hr, nh = min(hr, H - h0);
   const int each = (total + parts - 1) / parts, first = z * each, end = min(total, first + each);
   const int rounds = (each + W * R::NS - 1) / (W * R::NS);
-  const uint32_t rowb = 2u * (uint32_t)F;
+  const uint32_t rowb = 2u * (uint32_t)F, actb = 4u * (uint32_t)F;
   uint32_t avo[2 * NA];
 #pragma unroll
   for (int m = 0; m < 2 * NA; ++m)
     avo[m] = (lane >> 3) + 8 * m < nh ? (uint32_t)((lane >> 3) + 8 * m) * rowb + dma_piece(lane) : kOob;
-  // act: T k rows, and the second numbers' rows behind them
-  const uint32_t half = (uint32_t)(p.T * p.k) * rowb;
-  const rsrc_t ar = make_rsrc(p.act, 2 * half), none = make_rsrc(p.act, 0);
+  const rsrc_t ar = make_rsrc(p.act, (uint32_t)(p.T * p.k) * actb), none = make_rsrc(p.act, 0);
 
   int at = first + wave;          // the next loads: stage of all,
   int i = at / kst, s = at % kst;  // entry, stage of it
@@ -342,7 +374,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
     for (int c = 0; c < NT; ++c) {
       const int t = 16 * c + l16;
       on |= (mask >> t & 1) << c;
-      bvo[c] = mask >> t & 1 ? (uint32_t)(start + __popc(mask & ((1u << t) - 1))) * rowb + 16u * q : kOob;
+      bvo[c] = mask >> t & 1 ? (uint32_t)(start + __popc(mask & ((1u << t) - 1))) * actb + 32u * q : kOob;
     }
   };
   R g;
@@ -363,8 +395,8 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
       for (int c = 0; c < NT; ++c)
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-          g.b[u][2 * c][kk] = buf_load16(b, bvo[c], so + 64u * kk);
-          g.b[u][2 * c + 1][kk] = buf_load16(b, bvo[c] + half, so + 64u * kk);  // (kOob + half: still past every buffer)
+          g.b[u][2 * c][kk] = buf_load16(b, bvo[c], 2 * so + 128u * kk);
+          g.b[u][2 * c + 1][kk] = buf_load16(b, bvo[c] + 16u, 2 * so + 128u * kk);  // (kOob + 16: still past every buffer)
         }
       held = (held & ~(((1u << NT) - 1) << (u * NT))) | on << (u * NT);
       at += W;
@@ -374,21 +406,73 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
         seek();
       }
     };
-    // A stage's products; the sums of the tokens that its expert does not see stay as they
-    // were (zeros times a weight that is not finite would be NaN).
+    // A stage's products, in sums of their own, which the tokens that its expert does not
+    // see leave out (zeros times a weight that is not finite would be NaN).  f16: a
+    // token's 64 values are scaled by the power of two that brings the largest
+    // to [2^14, 2^15), so that its range holds them; what its parts cannot hold is below
+    // 2^-38 of that one.
     auto eat = [&](const lds_u8* from, int u) __attribute__((always_inline)) {
-      v4f old[NA][NT];
+      const auto weights = [&](int a, int kk) {
+        return *reinterpret_cast<const lds_v4i*>(from + a * 2048 + l16 * 128 + (((4 * kk + q) ^ (l16 & 7)) * 16));
+      };
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
+      for (int c = 0; c < NT; ++c) {
+        const auto largest = [&]() {
+          float m = 0.0f;
 #pragma unroll
-        for (int c = 0; c < NT; ++c) old[a][c] = g.acc[a][c];
-      consume(from, g, u);
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(__int_as_float(g.b[u][2 * c + i / 4 % 2][i / 8][i % 4])));
+          return m;
+        };
+        v4f sum[NA];
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
+        for (int a = 0; a < NA; ++a) sum[a] = v4f{0.f, 0.f, 0.f, 0.f};
+        float m = largest();
+        if (__ballot(m == INFINITY)) {  // infinities have no second part: their products apart
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
+          for (int kk = 0; kk < 2; ++kk) {
+            v4i inf = {0, 0, 0, 0};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) g.acc[a][c][e] = held >> (u * NT + c) & 1 ? g.acc[a][c][e] : old[a][c][e];
+            for (int e = 0; e < 8; ++e) {
+              const int v = g.b[u][2 * c + e / 4][kk][e % 4];
+              const bool is = (v & 0x7FFFFFFF) == 0x7F800000;
+              const uint32_t h = (uint32_t)v >> 31 << 15 | (TY == kBF16 ? 0x7F80u : 0x7C00u);
+              inf[e / 2] |= is ? (int)(h << (e % 2 * 16)) : 0;
+              g.b[u][2 * c + e / 4][kk][e % 4] = is ? 0 : v;
+            }
+#pragma unroll
+            for (int a = 0; a < NA; ++a) sum[a] = mfma16<TY>(weights(a, kk), inf, sum[a]);
+          }
+          m = largest();
+        }
+        float scale = 1.0f, back = 1.0f;
+        if (TY == kF16) {
+          const uint32_t e = max(__float_as_uint(max_of_quads(m)) >> 23, 15u);  // m = 2^(e - 127) to twice that
+          scale = __uint_as_float((268u - e) << 23);
+          back = __uint_as_float((e - 14u) << 23);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          float v[8];
+          v4i part[3];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __int_as_float(g.b[u][2 * c + e / 4][kk][e % 4]) * scale;
+          split<TY>(v, part);
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            const v4i w = weights(a, kk);
+#pragma unroll
+            for (int k = 2; k >= 0; --k) sum[a] = mfma16<TY>(w, part[k], sum[a]);
+          }
+        }
+        const bool see = held >> (u * NT + c) & 1;
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float old = g.acc[a][c][e];
+            g.acc[a][c][e] = see ? fmaf(sum[a][e], back, old) : old;
+          }
+      }
     };
     auto stages = [&](lds_u8* __restrict__ to, const lds_u8* __restrict__ from, bool first) __attribute__((always_inline)) {
       if (first) {

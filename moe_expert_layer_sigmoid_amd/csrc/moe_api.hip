@@ -571,7 +571,7 @@ int moe_forward_a16w16(const moe_dims_t* d, int32_t type, const int32_t* num_tok
   const moe_taps_t& tp = taps ? *taps : none;
   const FewLayout l = few_layout(d);
   const FewArgs p{x, logits, w1, w2, rep_count, rep_slots, num_tokens, load_hist, out, tp.topk_ids, tp.topk_w,
-                  tp.phys_ids, at<void>(ws, l.act), at<FewTable>(ws, 0), at<float>(ws, l.part), at<int32_t>(ws, l.cnt), d->T, d->H, d->F,
+                  tp.phys_ids, at<float>(ws, l.act), at<FewTable>(ws, 0), at<float>(ws, l.part), at<int32_t>(ws, l.cnt), d->T, d->H, d->F,
                   d->E, d->k, d->P_total, d->p0, d->P_local, d->R_max, d->token_id_base};
   return hip_status(launch_few(type, p, (hipStream_t)stream));
 }

@@ -173,8 +173,8 @@ hipError_t launch_gemm2_a16_pairs(const uint16_t* act, int T, int k, const int32
                                   int P_local, hipStream_t st);
 
 // The layer on 16-bit experts for T <= kFewMaxT tokens (kernels_a16w16.hip), type
-// 0 bf16 or 1 f16: w1 [P_local, 2F, H], w2 [P_local, H, F].  act: 2 T k rows of F
-// values; tab: few_table_bytes(); part: few_sums_bytes(T_max, H); cnt: kFewTiles
+// 0 bf16 or 1 f16: w1 [P_local, 2F, H], w2 [P_local, H, F].  act: T k rows of F
+// f32 values; tab: few_table_bytes(); part: few_sums_bytes(T_max, H); cnt: kFewTiles
 // counters.  t_dev, load_hist, ids, wts, phys may be null.
 constexpr int kFewMaxT = 32;
 struct FewTable;
@@ -188,7 +188,7 @@ struct FewArgs {
   int32_t* ids;
   float* wts;
   int32_t* phys;
-  void* act;
+  float* act;
   FewTable* tab;
   float* part;
   int32_t* cnt;

@@ -24,8 +24,8 @@ template <int TY>
 using Half = std::conditional_t<TY == kBF16, __bf16, _Float16>;
 
 // A wave's ring: NA tiles of 16 weight rows a stage, NS stages, and the token
-// operands of those stages in registers: NT tiles of 16 tokens, each held in P parts
-// whose sum is the value.
+// operands of those stages in registers: NT tiles of 16 tokens, a lane's eight values
+// of an MFMA in P words of 16 bytes.
 template <int TY, int NA, int NT, int P = 1>
 struct Ring {
   static constexpr int kSlot = NA * 2048;
@@ -41,8 +41,8 @@ struct Ring {
 // of a row permuted so that the reads spread over the LDS banks.
 __device__ __forceinline__ uint32_t dma_piece(int lane) { return 16u * (uint32_t)((lane & 7) ^ (lane >> 3)); }
 
-template <int TY, int NA, int NT, int P>
-__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT, P>& g, int u) {
+template <int TY, int NA, int NT>
+__device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT>& g, int u) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk)
@@ -50,7 +50,7 @@ __device__ __forceinline__ void consume(const lds_u8* rd, Ring<TY, NA, NT, P>& g
     for (int a = 0; a < NA; ++a) {
       const v4i w = *reinterpret_cast<const lds_v4i*>(rd + a * 2048 + l16 * 128 + (((4 * kk + q) ^ (l16 & 7)) * 16));
 #pragma unroll
-      for (int c = 0; c < NT * P; ++c) g.acc[a][c / P] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c / P]);
+      for (int c = 0; c < NT; ++c) g.acc[a][c] = mfma16<TY>(w, g.b[u][c][kk], g.acc[a][c]);
     }
 }
 
