@@ -6,6 +6,8 @@
 
 #include <type_traits>
 
+#include "gelu_tail.hpp"
+
 namespace moe {
 
 // e^-g from the hardware's exp2 (1 ulp), its argument carried in two parts:
@@ -44,22 +46,14 @@ enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4,
 constexpr float kGeluC = 0.797884561f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// Phi(-a) e^(a^2 / 2) for a >= 0, as t Q(t) with t = 1 / (1 + 0.27 a): Q of degree 8
-// fitted to the scaled complementary error function for the least largest relative
-// error over 0 <= a <= 27 (4.9e-8; with f32's roundings 8 x 2^-24).  One exponential then
-// gives Phi and phi both, and the negative tail keeps its relative error.  (erfcf
-// bound the gradient by its arithmetic: 29343 rows x 672, 46 us for 31.)
+// Phi(-a) e^(a^2 / 2) for a >= 0 (gelu_tail.hpp).  One exponential then gives Phi and phi
+// both, and the negative tail keeps its relative error.  (erfcf bound the gradient by its
+// arithmetic: 29343 rows x 672, 46 us for 31.)
 __device__ __forceinline__ float scaled_tail(float a) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.27f, a, 1.0f));
-  float q = 0.0279833451f;
-  q = fmaf(q, t, -0.122192788f);
-  q = fmaf(q, t, 0.161887512f);
-  q = fmaf(q, t, -0.0613035224f);
-  q = fmaf(q, t, 0.103147648f);
-  q = fmaf(q, t, 0.0737099299f);
-  q = fmaf(q, t, 0.101469174f);
-  q = fmaf(q, t, 0.107579507f);
-  q = fmaf(q, t, 0.107719123f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(kTailArg, a, 1.0f));
+  float q = kTail[kTailDegree];
+#pragma unroll
+  for (int i = kTailDegree - 1; i >= 0; --i) q = fmaf(q, t, kTail[i]);
   return t * q;
 }
 // e^(-z^2 / 2) for z >= -13 and beyond any normal value above

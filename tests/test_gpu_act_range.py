@@ -1,0 +1,80 @@
+"""GPU tests of the activations and their slopes where their formulas are hard: at
+zero, far out, at infinity.  Against the float64 oracle, in f32 outputs.
+
+Forward: x is zero and the bias is z, so that z is what the test says, to the bit, in
+the kernel of few rows, in tiles and in joined splits.  Gradient: every row is a group of
+its own, so that db holds the row's f32 values before they are rounded to dz.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_layer_sigmoid_amd as mx
+from oracle import experts as oe
+
+pytestmark = pytest.mark.gpu
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _pad(v, n):
+    """v (a list) as n values: repeated from the front."""
+    return torch.tensor([v[i % len(v)] for i in range(n)], dtype=torch.float32)
+
+
+FORWARD = [(3, 64), (40, 64), (40, 4104)]   # rows, K: few rows, tiles, joined splits
+
+
+def forward(act, z, u=None, rows=3, K=64):
+    """act(z) [* u], f32; z and u 1-D, of values that bf16 holds."""
+    b = (z if u is None else torch.cat([z, u])).bfloat16().cuda()[None].contiguous()
+    N = b.shape[1]
+    d = mx.Linear(rows, N, K, out_type="f32")
+    x, w = torch.zeros(rows, K, device="cuda").bfloat16(), torch.zeros(1, N, K, device="cuda").bfloat16()
+    y = torch.full((rows, len(z)), 7.0, device="cuda")
+    mx.moe_grouped_linear_act(d, x, w, y, mx.linear_act_workspace(d), act=act, gated=u is not None, bias=b)
+    assert torch.equal(y.nan_to_num(1.5), y[:1].nan_to_num(1.5).expand_as(y))
+    return y[0].cpu()
+
+
+def backward(act, z, dy, u=None, rows=2):
+    """The f32 gradient of z [and of u] for dy, all 1-D f32 (dz's rounding left out)."""
+    pre = (z if u is None else torch.cat([z, u])).cuda()[None].expand(rows, -1).contiguous()
+    N = pre.shape[1]
+    d = mx.Linear(rows, N, 64, groups=rows, out_type="f32")
+    off = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+    dz, db = torch.empty(rows, N, device="cuda").bfloat16(), torch.empty(rows, N, device="cuda")
+    mx.moe_grouped_linear_act_backward(d, dy.cuda()[None].expand(rows, -1).contiguous(), pre, dz, mx.linear_act_workspace(d),
+                                       act=act, gated=u is not None, db=db, offsets=off)
+    assert torch.equal(db.nan_to_num(1.5), db[:1].nan_to_num(1.5).expand_as(db))
+    assert torch.equal(dz.nan_to_num(1.5), db.bfloat16().nan_to_num(1.5))
+    return db[0].cpu()
+
+
+BACKWARD = [2, 300]   # rows: one launch, two
+
+
+@pytest.mark.parametrize("rows", BACKWARD)
+def test_slopes_at_zero(rows):
+    """Half of one, but for none and relu: exactly."""
+    z = _pad([0.0, -0.0], 16)
+    for act, want in (("none", 1.0), ("relu", 0.0), ("silu", 0.5), ("gelu", 0.5), ("gelu_tanh", 0.5)):
+        got = backward(act, z, torch.full((16,), 3.0), rows=rows)
+        assert torch.all(got == 3.0 * want), (act, got)
+        got = backward(act, z, torch.full((16,), 3.0), torch.full((16,), -2.0), rows=rows)
+        assert torch.all(got[:16] == -6.0 * want) and torch.all(got[16:] == 0.0), (act, got)
+
+
+@pytest.mark.parametrize("rows,K", FORWARD)
+def test_gelu_of_small_values(rows, K):
+    """z Phi(z) to the tail's 6 x 2^-24, the reciprocal's and the exponential's ulps (2 x
+    2^-24 each, three of the exponential's) and the products' roundings (3)."""
+    z = torch.cat([torch.logspace(-30, -1, 60), torch.linspace(0.1, 1.0, 68)]).bfloat16().float()
+    z = torch.cat([z, -z])
+    y = _np(forward("gelu", z, rows=rows, K=K))
+    ref = oe.act("gelu", z.double().numpy())
+    rel = np.abs(y / ref - 1)
+    assert np.all(rel <= (6 + 2 + 3 * 2 + 3) * oe.U), rel.max() / oe.U
