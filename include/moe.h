@@ -493,7 +493,9 @@ int moe_grouped_linear_act(const moe_linear_t* d, int32_t act, int32_t gated, co
  * dy [rows, N], gated [rows, N / 2], and pre [rows, N] of out_type; dz [rows, N]
  * of in_type, what moe_grouped_linear_dx and _dw take as dy; db (nullable) f32
  * [groups, N], overwritten, added up from the f32 values before their rounding.
- * (The residual's gradient is dy.)  relu'(0) = 0.  N a multiple of 8; K is not
+ * (The residual's gradient is dy.)  relu'(0) = 0.  An infinite z gives what the
+ * formulas give, as above: NaN for silu, gelu and gelu_tanh, but act(inf) = inf.  N a
+ * multiple of 8; K is not
  * used but must be valid.  dz may be pre itself where the types are the same.
  * The workspace is needed for db alone.  One launch; for db of more rows than
  * a few blocks can add up (256 at most), two. */

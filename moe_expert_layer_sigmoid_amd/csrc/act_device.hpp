@@ -138,7 +138,8 @@ __device__ __forceinline__ void act_gated(const float (&z)[G][V], float (&v)[V])
 //  silu:      s = sigmoid(z): z s and s (1 + z (1 - s)), 1 - s = e s
 //  gelu:      z Phi(z) and Phi(z) + z phi(z)
 //  gelu_tanh: s = sigmoid(t), t = 2 w: z s and s + z s (1 - s) t'(z); beyond 16 the
-//             slope is 1 or 0 in f32, and z^2 would overflow
+//             slope is 1 or 0 in f32, and t' would overflow
+// An infinite z gives NaN where the formula has 0 times infinity (z phi(z), z (1 - s)).
 // For z >= far_below<ACT>(); below: grad_far.
 template <int ACT>
 __device__ __forceinline__ void act_slope(float z, float& f, float& d) {
@@ -158,7 +159,7 @@ __device__ __forceinline__ void act_slope(float z, float& f, float& d) {
     const float x2 = x * x, t = 2.0f * kGeluC * x * fmaf(kGeluA, x2, 1.0f);
     const float e = t > 88.0f ? 0.0f : exp_neg(t < -80.0f ? -80.0f : t), s = __builtin_amdgcn_rcpf(1.0f + e);
     f = z * s;
-    d = s * fmaf(x * (e * s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f);
+    d = s * fmaf(z * (e * s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f);
   } else {
     f = z;
     d = 1.0f;
@@ -166,7 +167,8 @@ __device__ __forceinline__ void act_slope(float z, float& f, float& d) {
 }
 // dz and df for z < far_below<ACT>(): v act'(z) and w act(z), e^t in four factors
 // (silu: act' = e^z (1 + z); gelu: e^(-z^2 / 2) (scaled tail + z / sqrt(2 pi));
-// gelu_tanh: e^t (1 + z t'(z)); 1 - s is 1 there).
+// gelu_tanh: e^t (1 + z t'(z)); 1 - s is 1 there).  z - z: both are NaN for z = -inf,
+// which the bounds on x hide (silu's t is 0 there, and 0 times z is NaN already).
 template <int ACT>
 __device__ __forceinline__ void grad_far(float z, float v, float w, float& dz, float& df) {
   if constexpr (ACT == kActSilu) {
@@ -176,13 +178,13 @@ __device__ __forceinline__ void grad_far(float z, float v, float w, float& dz, f
   } else if constexpr (ACT == kActGelu) {
     float x = z;
     const float t = gauss_root(x), c = scaled_tail(-x);
-    dz = (fmaf(x, kPhi0, c) * t) * (v * t) * t * t;
-    df = (x * c * t) * (w * t) * t * t;
+    dz = (fmaf(x, kPhi0, c) * t) * (v * t) * t * t + (z - z);
+    df = (x * c * t) * (w * t) * t * t + (z - z);
   } else if constexpr (ACT == kActGeluTanh) {
     const float x = z < -20.0f ? -20.0f : z, x2 = x * x;  // t(-20) = -603: zero
     const float t = exp_neg(-0.5f * kGeluC * x * fmaf(kGeluA, x2, 1.0f));
-    dz = (fmaf(x * 2.0f * kGeluC, fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f) * t) * (v * t) * t * t;
-    df = (x * t) * (w * t) * t * t;
+    dz = (fmaf(x * 2.0f * kGeluC, fmaf(3.0f * kGeluA, x2, 1.0f), 1.0f) * t) * (v * t) * t * t + (z - z);
+    df = (x * t) * (w * t) * t * t + (z - z);
   }
 }
 

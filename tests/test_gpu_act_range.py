@@ -78,3 +78,36 @@ def test_gelu_of_small_values(rows, K):
     ref = oe.act("gelu", z.double().numpy())
     rel = np.abs(y / ref - 1)
     assert np.all(rel <= (6 + 2 + 3 * 2 + 3) * oe.U), rel.max() / oe.U
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+def _same(got, want):
+    want = torch.tensor(want)
+    return torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(0.5, INF, -INF), want.nan_to_num(0.5, INF, -INF))
+
+
+@pytest.mark.parametrize("rows,K", FORWARD)
+def test_infinite_z_forward(rows, K):
+    """What the formula gives: 0 times infinity is NaN."""
+    z, u = _pad([INF, -INF, NAN, 1.0], 16), _pad([-2.0] * 16, 16)
+    want = {"none": [INF, -INF], "relu": [INF, 0.0], "silu": [INF, NAN], "gelu": [INF, NAN], "gelu_tanh": [INF, NAN]}
+    for act, v in want.items():
+        assert _same(forward(act, z, rows=rows, K=K)[:3], v + [NAN]), act
+        assert _same(forward(act, z, u, rows=rows, K=K)[:3], [-2.0 * a for a in v] + [NAN]), act
+
+
+@pytest.mark.parametrize("rows", BACKWARD)
+def test_infinite_z_in_the_gradient(rows):
+    """Slopes hold z times phi(z), or z times 1 - sigmoid: NaN at both ends."""
+    z, dy, u = _pad([INF, -INF, 1.0, 2.0], 16), _pad([3.0, 3.0, 0.5, 0.25], 16), _pad([-2.0] * 16, 16)
+    slope = {"none": [1.0, 1.0], "relu": [1.0, 0.0], "silu": [NAN, NAN], "gelu": [NAN, NAN], "gelu_tanh": [NAN, NAN]}
+    value = {"none": [INF, -INF], "relu": [INF, 0.0], "silu": [INF, NAN], "gelu": [INF, NAN], "gelu_tanh": [INF, NAN]}
+    for act in slope:
+        got = backward(act, z, dy, rows=rows)
+        assert _same(got[:2], [3.0 * a for a in slope[act]]), (act, got)
+        gated = backward(act, z, dy, u, rows=rows)
+        assert _same(gated[:2], [-6.0 * a for a in slope[act]]), (act, gated)
+        assert _same(gated[16:18], [3.0 * a for a in value[act]]), (act, gated)
+        assert torch.isfinite(got[2:4]).all() and torch.isfinite(gated[2:4]).all()
