@@ -527,8 +527,9 @@ size_t moe_grad_workspace_bytes(int32_t count);
 int moe_grad_norm(const moe_tensor_t* tensors, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
                   moe_stream_t stream);
 
-/* out = in * min(1, max_norm / (norm + 1e-6)), rounded once; norm (nullable)
- * receives the norm before.  max_norm >= 0.  A NaN among the values makes every
+/* out = in * min(1, max_norm / (norm + 1e-6)), the factor and the product in f64,
+ * rounded to f32 and from there to a 16-bit type; norm (nullable, f32) receives the norm
+ * before.  max_norm >= 0.  A NaN among the values makes every
  * output NaN; an infinity makes the factor 0 (and itself NaN).  2 ceil(count / 168)
  * launches. */
 int moe_grad_clip(const moe_tensor_t* tensors, int32_t count, float max_norm, float* norm, void* workspace,

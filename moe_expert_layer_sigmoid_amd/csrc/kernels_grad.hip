@@ -179,13 +179,12 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(Table t, const double* 
   const Run run(t, true);  // on its way while the norm is added up
   const double v = norm_of(part, parts);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-  const double q = max_norm / (v + 1e-6);
-  // a NaN norm gives NaN, an infinite one 0; a factor near or below f32's normal
-  // range keeps its bits by a power of two apart
-  const float scale = q < 0x1p-64 ? 0x1p-64f : 1.0f;
-  const float c = q > 1.0 ? 1.0f : (float)(q / scale);
+  // (a NaN norm gives NaN, an infinite one 0)  The factor and its products are f64, which
+  // has the range for any of them: rounded to f32 first, the factor would bring as much
+  // error as the product's own rounding, and more below f32's normal range.
+  const double q = max_norm / (v + 1e-6), c = q > 1.0 ? 1.0 : q;
   chunks(t, run, true, [&](int i, int64_t e0, int n, int type) {
-    if (c == 1.0f && t.in[i] == t.out[i]) return;  // nothing to change
+    if (c == 1.0 && t.in[i] == t.out[i]) return;  // nothing to change
     with_type(type, [&](auto tc) {
       constexpr int T = decltype(tc)::value;
       using E = Elem<T>;
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(Table t, const double* 
         constexpr int V = 16 / sizeof(E);
         E x[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = (E)((float)v[e] * c * scale);
+        for (int e = 0; e < V; ++e) x[e] = (E)(float)((double)(float)v[e] * c);
         if (m == V) {
           v4i w;
           __builtin_memcpy(&w, x, 16);
