@@ -12,6 +12,7 @@ import torch
 
 import moe_expert_layer_sigmoid_amd as mx
 from oracle import experts as oe
+from tests.test_gpu_linear_act import Back
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +112,66 @@ def test_infinite_z_in_the_gradient(rows):
         assert _same(gated[:2], [-6.0 * a for a in slope[act]]), (act, gated)
         assert _same(gated[16:18], [3.0 * a for a in value[act]]), (act, gated)
         assert torch.isfinite(got[2:4]).all() and torch.isfinite(gated[2:4]).all()
+
+
+# Both sides of where the exponentials leave f32's normal range (-80, -13, -9), as far as a
+# factor of 1e30 brings the product back.
+FAR = {"silu": np.linspace(-150.0, -70.0, 161), "gelu": np.linspace(-16.5, -10.0, 131), "gelu_tanh": np.linspace(-12.5, -7.0, 111)}
+
+
+@pytest.mark.parametrize("rows,K", FORWARD)
+@pytest.mark.parametrize("act", list(FAR))
+def test_far_values(act, rows, K):
+    z = torch.tensor(FAR[act]).bfloat16().float()
+    u = torch.cat([torch.full_like(z, v) for v in (1.0, -1e15, 1e30)]).bfloat16().float()
+    z = torch.cat([z, z, z])
+    n = len(z)
+    got = _np(forward(act, z, u, rows=rows, K=K))
+    zd, ud = z.double().numpy(), u.double().numpy()
+    ref = oe.act(act, zd) * ud
+    tol = (oe.act_rel(act, zd) + oe.U) * np.abs(ref) + 2.0 ** -126
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (zd[bad][:4], ud[bad][:4], got[bad][:4], ref[bad][:4])
+    assert np.sum(np.abs(ref) > 2.0 ** -120) > n // 3   # (not for want of normal values)
+    alone = _np(forward(act, z, rows=rows, K=K))
+    ref = oe.act(act, zd)
+    assert np.all(np.abs(alone - ref) <= oe.act_rel(act, zd) * np.abs(ref) + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("rows", BACKWARD)
+@pytest.mark.parametrize("act", list(FAR))
+def test_far_gradients(act, rows):
+    z = torch.tensor(FAR[act], dtype=torch.float32)
+    z = torch.cat([z, z, z])
+    n = len(z) // 24 * 8   # of each factor
+    z = torch.cat([z[:n], z[:n], z[:n]])
+    dy = torch.cat([torch.full((n,), v) for v in (1.0, -1e15, 1e30)])
+    zd, dd = z.double().numpy(), dy.double().numpy()
+    got = _np(backward(act, z, dy, rows=rows))
+    ref = oe.slope(act, zd) * dd
+    tol = np.abs(dd) * oe.slope_tol(act, zd) + 2 * oe.U * np.abs(ref) + 2.0 ** -126
+    assert np.all(np.abs(got - ref) <= tol), (got, ref)
+    assert np.sum(np.abs(ref) > 2.0 ** -120) > n
+    # gated: the factor in up (the value's gradient then takes dy), or in dy
+    for d, u in ((torch.full_like(dy, 0.75), dy), (dy, torch.full_like(dy, -1.25))):
+        got = _np(backward(act, z, d, u, rows=rows))
+        d, u = d.double().numpy(), u.double().numpy()
+        gate, up = oe.slope(act, zd) * d * u, oe.act(act, zd) * d
+        tol = np.abs(d * u) * (oe.slope_tol(act, zd) + 2 * oe.U * np.abs(oe.slope(act, zd))) + 2.0 ** -126
+        assert np.all(np.abs(got[:len(z)] - gate) <= tol), (got[:len(z)], gate)
+        tol = (oe.act_rel(act, zd) + 2 * oe.U) * np.abs(up) + 2.0 ** -126
+        assert np.all(np.abs(got[len(z):] - up) <= tol), (got[len(z):], up)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,groups,N", [(4000, 3, 264), (9000, 1, 4112), (3000, 40, 72)])
+def test_gradient_in_place_of_long_tiles(rows, groups, N, gated):
+    """dz over pre where a thread has four rows in flight, the last of them read twice."""
+    c = Back(rows, groups, N, "silu", gated)
+    c.check()
+    clean = c.db.clone()
+    z = c.pre.clone()
+    c.db.fill_(7.0)
+    c.run(dz=z, pre=z)
+    torch.cuda.synchronize()
+    assert torch.equal(z, c.dz) and torch.equal(c.db, clean)
