@@ -13,7 +13,7 @@
 // is lost (rounded once to 16 bits, it would bring as much error as the output's own
 // rounding: normwise 0.0024 for 0.0017 in bf16; in two 16-bit parts, f16's range ended
 // at 65504.  Parted in each block as it is used: both launches for 32 tokens on 48 of
-// 384 experts 312 us, f16 323, for 303 with two parts stored).
+// 384 experts 305 us, f16 307, for 303 with two parts stored).
 // MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
 // experts' weights, streamed as ring.hpp says: H 7168, F 2048, bf16, one token on 6
 // experts 57 + 31 us (6.2 and 5.8 TB/s), 16 tokens on 42 375 + 183 (6.7 and 6.9).
@@ -417,6 +417,8 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
       };
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
+        const bool see = held >> (u * NT + c) & 1;
+        if (NT > 1 && !__ballot(see)) continue;  // none of the tile's tokens (the 305 us above were 312)
         const auto largest = [&]() {
           float m = 0.0f;
 #pragma unroll
@@ -464,7 +466,6 @@ __global__ void __launch_bounds__(kDownWaves * 64, 2) k_few_down(FewArgs p, int 
             for (int k = 2; k >= 0; --k) sum[a] = mfma16<TY>(w, part[k], sum[a]);
           }
         }
-        const bool see = held >> (u * NT + c) & 1;
 #pragma unroll
         for (int a = 0; a < NA; ++a)
 #pragma unroll
