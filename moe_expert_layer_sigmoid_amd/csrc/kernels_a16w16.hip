@@ -16,7 +16,7 @@
 // 384 experts 305 us, f16 307, for 303 with two parts stored).
 // MFMA columns are tokens (16 a tile), rows are weight rows.  Bound by the touched
 // experts' weights, streamed as ring.hpp says: H 7168, F 2048, bf16, one token on 6
-// experts 57 + 31 us (6.2 and 5.8 TB/s), 16 tokens on 42 375 + 183 (6.7 and 6.9).
+// experts 57 + 32 us (6.2 and 5.4 TB/s), 16 tokens on 43 371 + 190 (6.8 and 6.7).
 
 #include <hip/hip_runtime.h>
 
@@ -35,8 +35,8 @@ constexpr int kPairs = kFewMaxT * 16;  // T k at most
 
 // The touched slots, ascending; the pairs of an entry are act rows [start, start +
 // popc(mask)), one per bit (token) of mask, ascending.  A slot with more than 16 tokens
-// is two entries (its weights are then read twice, the second time mostly from
-// a cache).
+// is two entries, and its weights are then read twice (H 7168, F 2048, all tokens on
+// 8 experts: 16 tokens 131 us, 32 241).
 struct FewTable {
   int n;
   int pad[3];

@@ -1,6 +1,6 @@
-// The weight stream of the kernels for few token rows: a block of four waves takes
-// 16 weight rows (or twice that), each wave every fourth 128-byte piece of the
-// reduction.  The weights come by DMA, in whole lines, into an LDS ring that
+// The weight stream of the kernels for few token rows: a block of four or eight waves
+// takes 16 weight rows (or twice that), each wave every fourth or eighth 128-byte piece of
+// the reduction.  The weights come by DMA, in whole lines, into an LDS ring that
 // belongs to one wave alone: no wave waits for another but at the end of a
 // block's rows, and the next rows' weights are then already on their way.  The token
 // operand (a few KB, from L2) is loaded straight into registers as far ahead.
@@ -15,9 +15,8 @@
 namespace moe {
 namespace {
 
-constexpr int kRingWaves = 4;
-constexpr int kRingThreads = kRingWaves * 64;
-constexpr int kRingBytes = 16384;  // of a wave: two blocks a compute unit
+constexpr int kRingWaves = 4;      // of a block, two blocks a compute unit; or eight, one block
+constexpr int kRingBytes = 16384;  // of a wave
 constexpr int kStageK = 64;        // reduction elements of a stage: 128 bytes of a row
 
 template <int TY>
@@ -71,7 +70,7 @@ __device__ __forceinline__ void burst(lds_u8* mine, int per, Issue issue, Eat ea
 
 // The W waves' sums of acc[a][c], by thread of the first four waves (token column
 // tid / 16, weight row tid % 16).
-template <int NA, int W = kRingWaves>
+template <int NA, int W>
 __device__ __forceinline__ void reduce(float (*red)[NA][256], const v4f (&v)[NA], float (&s)[NA]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 #pragma unroll

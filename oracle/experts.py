@@ -138,9 +138,11 @@ def clip(grads, max_norm):
 
 def layer(x, w1, w2, phys, topk_w, p0, eps):
     """The layer on the pairs (t, j) of phys / topk_w [T, k]: (out, its bound
-    before the output's rounding).  eps: of the operands' type, in two numbers of
-    which w * act is held (half a step of the second: eps^2 / 4, and half of f16's
-    smallest number); topk_w: float64 weights, 4e-6 of their value uncertain."""
+    before the output's rounding).  w * act is held in f32 and enters the second
+    product in three parts, which lose nothing above f32's smallest normal number, in f16
+    (eps 2^-10) nothing above 2^-38 of the largest of 64 columns; sums of three products a
+    column, and of one value every 64 columns.  topk_w: float64 weights, 4e-6 of their
+    value uncertain."""
     T, H = x.shape
     F = w2.shape[2]
     out, tol, mag = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
@@ -157,8 +159,12 @@ def layer(x, w1, w2, phys, topk_w, p0, eps):
             f, w = act("silu", a), topk_w[t, j]
             v = f * u * w
             tv = w * (1.1 * th[:F] * (np.abs(u) + th[F:]) + np.abs(f) * th[F:]) + (24 * U + 4e-6) * np.abs(v)
-            tv += eps * eps / 4 * (np.abs(v) + tv) + 2.0 ** -25
+            tv += 2.0 ** -126
+            if eps == 2.0 ** -10:
+                top = np.maximum.reduceat(np.abs(v) + tv, np.arange(0, F, 64))
+                tv += 2.0 ** -38 * np.repeat(top, 64)[:F]
             out[t] += w2[s] @ v
             tol[t] += np.abs(w2[s]) @ tv
             mag[t] += np.abs(w2[s]) @ (np.abs(v) + tv)
-    return out, tol + ol.sum_bound(2 * F * max(pairs, 1)) * mag
+    n = F * max(pairs, 1)
+    return out, tol + ol.sum_bound(3 * n + n // 8) * mag   # (four roundings for 32 products: n / 64 sums are as 8 n / 64)
