@@ -494,10 +494,9 @@ int moe_grouped_linear_act(const moe_linear_t* d, int32_t act, int32_t gated, co
  * of in_type, what moe_grouped_linear_dx and _dw take as dy; db (nullable) f32
  * [groups, N], overwritten, added up from the f32 values before their rounding.
  * (The residual's gradient is dy.)  relu'(0) = 0.  An infinite z gives what the
- * formulas give, as above: NaN for silu, gelu and gelu_tanh, but act(inf) = inf.  N a
- * multiple of 8; K is not
- * used but must be valid.  dz may be pre itself where the types are the same.
- * The workspace is needed for db alone.  One launch; for db of more rows than
+ * formulas give, as above: NaN for silu, gelu and gelu_tanh, but act(inf) = inf.  N
+ * a multiple of 8; K is not used but must be valid.  dz may be pre itself where the
+ * types are the same.  The workspace is needed for db alone.  One launch; for db of more rows than
  * a few blocks can add up (256 at most), two. */
 int moe_grouped_linear_act_backward(const moe_linear_t* d, int32_t act, int32_t gated, const void* dy, const void* pre,
                                     const int32_t* offsets, void* dz, float* db, void* workspace,
@@ -528,10 +527,9 @@ int moe_grad_norm(const moe_tensor_t* tensors, int32_t count, float* norm, void*
                   moe_stream_t stream);
 
 /* out = in * min(1, max_norm / (norm + 1e-6)), the factor and the product in f64,
- * rounded to f32 and from there to a 16-bit type; norm (nullable, f32) receives the norm
- * before.  max_norm >= 0.  A NaN among the values makes every
- * output NaN; an infinity makes the factor 0 (and itself NaN).  2 ceil(count / 168)
- * launches. */
+ * rounded to f32 and from there to a 16-bit type; norm (nullable, f32) receives the
+ * norm before.  max_norm >= 0.  A NaN among the values makes every output NaN; an
+ * infinity makes the factor 0 (and itself NaN).  2 ceil(count / 168) launches. */
 int moe_grad_clip(const moe_tensor_t* tensors, int32_t count, float max_norm, float* norm, void* workspace,
                   size_t workspace_bytes, moe_stream_t stream);
 
